@@ -1,8 +1,9 @@
 /*
  * pa.h -- C ABI of the paged KV-cache library for NVIDIA B200 (sm_100a):
  * decode, split-K decode, slot write fused with decode, prefill, slot writes
- * and block copies (16-bit, fp32 and int8 caches), the host block pool with
- * its prefix cache, and a device block pool with a beam-search step.
+ * and block copies (16-bit, fp32 and int8 caches, the latter with a scale per
+ * row or per block), the host block pool with its prefix cache, and a device
+ * block pool with append, release and a beam-search step.
  *
  * A sequence's keys and values live in fixed-size blocks of a shared pool; a
  * per-sequence block table maps logical block i (tokens i*bs .. i*bs+bs-1) to
@@ -581,6 +582,122 @@ int pa_beam_step_withhold_arrival(void *state, int num_blocks, int block_size, c
                                   int32_t *new_tables, int32_t *new_context_lens, int max_blocks_per_seq,
                                   int32_t *slot_mapping, int64_t *cow_pairs, int32_t *num_cow, int cta,
                                   unsigned long long wait_limit_ns, cudaStream_t stream);
+
+/*
+ * pa_dpool_append -- block tables, context lengths, query starts, slot map
+ * and copy-on-write pairs of a serving step, made on the device from the
+ * lengths ([P2] §3.3 and §4.2; [P4] §3.3). Sequence s, which holds
+ * context_lens[s] tokens, appends new_lens[s] >= 0 of them; the result is
+ * that of pa_pool_append over the sequences in order: a token at a block
+ * boundary takes a free block; the first token into a partly filled block
+ * whose count is above 1 takes a free block, drops the old block's count and
+ * gives the pair (old, new) to copy.
+ * In and out (device): block_tables [num_seqs, max_blocks_per_seq] (the new
+ * entries are written, others are left; entries past the blocks in use are
+ * not read) and context_lens [num_seqs] (new_lens is added). Outputs
+ * (device): q_start [num_seqs + 1], the exclusive sums of new_lens;
+ * slot_mapping [max_tokens], the new tokens' slots, sequence by sequence,
+ * then -1; cow_pairs int64 [num_seqs, 2] (16-byte aligned), *num_cow pairs in
+ * sequence order, then (-1, -1). So q_start is pa_prefill's and
+ * pa_append_q8b's, slot_mapping pa_reshape_and_cache's (which skips the
+ * padding) and the pairs those of the counted block copies, without the host
+ * knowing how many there are; every buffer has a fixed size, so the step can
+ * be captured in a CUDA graph.
+ * Any error (a negative length, a context or the new tokens past the table
+ * row, a bad block id, a free list too short, more than max_tokens tokens, an
+ * uninitialised state or one of other sizes) applies nothing: the pool, the
+ * tables and the lengths are unchanged, q_start is all 0, every slot and pair
+ * -1, *num_cow = 0 and a PA_DEVERR_* bit is set. The arrays must not overlap.
+ * One launch; num_seqs <= PA_DPOOL_MAX_SEQS and num_seqs * max_blocks_per_seq
+ * < 2^30 (else PA_ERR_SHAPE). Calls on one state must not overlap.
+ */
+#define PA_DPOOL_MAX_SEQS 8192
+int pa_dpool_append(void *state, int num_blocks, int block_size, int32_t *block_tables, int max_blocks_per_seq,
+                    int32_t *context_lens, const int32_t *new_lens, int num_seqs, int32_t *q_start,
+                    int32_t *slot_mapping, int max_tokens, int64_t *cow_pairs, int32_t *num_cow,
+                    cudaStream_t stream);
+
+/*
+ * pa_dpool_release -- returns the blocks of finished sequences on the device.
+ * For every sequence s with finished[s] != 0 (device int32 [num_seqs]), in
+ * order: pa_pool_release of its blocks (each table entry in order drops the
+ * block's count; a block reaching 0 goes to the free list's back); its
+ * entries in use become -1 and context_lens[s] 0. Other sequences are left.
+ * Any error (a context past the table row, a bad block id, more drops than a
+ * block's count, an uninitialised state or one of other sizes) applies
+ * nothing and sets a PA_DEVERR_* bit. Sizes, layouts and limits as
+ * pa_dpool_append.
+ */
+int pa_dpool_release(void *state, int num_blocks, int block_size, int32_t *block_tables, int max_blocks_per_seq,
+                     int32_t *context_lens, const int32_t *finished, int num_seqs, cudaStream_t stream);
+
+/*
+ * int8 KV caches with one scale per (block, kv head): half the bytes of a
+ * 16-bit cache, and 1/block_size as many scales as the row-scaled cache
+ * above (whose scheme stays as it is; [P4] §3.4, [P2] §2.3 name int8 storage
+ * without a scheme, this one is the library's too).
+ * Layouts: k_cache/v_cache int8 [num_blocks, num_kv_heads, block_size,
+ * head_dim]; k_scale/v_scale fp32 [num_blocks, num_kv_heads]; all 16-byte
+ * aligned. Token t of block b holds K_t = q_t * k_scale[b, h].
+ */
+
+/*
+ * pa_append_q8b -- quantizing write of each sequence's newest tokens. The
+ * q_len_s = q_start[s + 1] - q_start[s] new tokens of sequence s (rows
+ * q_start[s] .. of key and value [num_tokens, num_kv_heads, head_dim], of
+ * src_dtype PA_F32, PA_F16 or PA_BF16) are its last ones: positions
+ * context_lens[s] - q_len_s .. context_lens[s] - 1, through its block table.
+ * For each (block, head) that gets rows, K and V on their own, every step one
+ * IEEE fp32 operation:
+ *   new = amax / 127 over the rows' finite |x|, 0 below FLT_MIN;
+ *   s   = max(old, new) if older tokens of the sequence live in the block
+ *         (old: its scale so far), else new;
+ *   q   = round_half_even(x * (1 / s)) clamped to [-127, 127]; 0 where s = 0
+ *         or x is NaN (+-inf gives +-127);
+ *   if s > old and older tokens live there, their codes become
+ *   round_half_even(q * (old / s)).
+ * So a token's row is off by half a step of its block's scale, and by at most
+ * half a step more for every later token that raised that scale. Rows of key
+ * and value from q_start[num_seqs] on are not read (a padded batch); slots of
+ * a block past the sequence's last token are left as they were. No other
+ * sequence may hold a block that is written (true once copy-on-write has
+ * given each sequence its own last block). q_start must be non-decreasing
+ * from 0 and at most num_tokens at its end. A sequence with q_len_s >
+ * context_lens[s] or a context past its table row is skipped
+ * (PA_DEVERR_CONTEXT), a block with a bad id as well (PA_DEVERR_BLOCK_ID).
+ */
+int pa_append_q8b(const void *key, const void *value, pa_dtype src_dtype, const int32_t *q_start, int num_tokens,
+                  int8_t *k_cache, int8_t *v_cache, float *k_scale, float *v_scale, const int32_t *block_tables,
+                  int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_blocks,
+                  int num_kv_heads, int head_dim, int block_size, cudaStream_t stream);
+
+/*
+ * pa_decode_q8b -- pa_decode over that cache: out = softmax(scale q . K_t)
+ * V_t with K_t = kq_t * k_scale[block, h], V_t = vq_t * v_scale[block, h].
+ * query is q_dtype (PA_F16 or PA_BF16); out_dtype q_dtype or PA_F32.
+ * max_context_len bounds every context_lens[s] (longer ones are clamped,
+ * PA_DEVERR_CONTEXT). workspace (nullable device buffer, 16-byte aligned, of
+ * at least pa_decode_q8b_workspace_bytes, else PA_ERR_WORKSPACE) lets a batch
+ * of few, long sequences be split along the tokens over more CTAs and joined;
+ * without it each (sequence, kv head) is one CTA's work. Its contents need no
+ * initialisation and mean nothing after the call; calls that may run at the
+ * same time must not share one. Other arguments, checks and device errors as
+ * pa_decode.
+ */
+size_t pa_decode_q8b_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                     int max_context_len);
+int pa_decode_q8b(void *out, const void *query, pa_dtype q_dtype, const int8_t *k_cache, const int8_t *v_cache,
+                  const float *k_scale, const float *v_scale, const int32_t *block_tables, int max_blocks_per_seq,
+                  const int32_t *context_lens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                  float scale, int block_size, int num_blocks, int max_context_len, pa_dtype out_dtype,
+                  const int32_t *seq_order, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* pa_copy_blocks for that cache: codes and scales of each pair. num_pairs
+ * (nullable device int32): only the first *num_pairs of max_pairs pairs, as
+ * pa_copy_blocks_counted. */
+int pa_copy_blocks_q8b(int8_t *k_cache, int8_t *v_cache, float *k_scale, float *v_scale,
+                       const int64_t *src_dst_pairs, const int32_t *num_pairs, int max_pairs, int num_blocks,
+                       int num_kv_heads, int head_dim, int block_size, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -13,15 +13,17 @@ split-K decode and reduce (pa_decode_splitk, pa_splitk_reduce,
 pa_decode_splitk_static),
 copy-on-write block copy (pa_copy_blocks, pa_copy_blocks_counted), paged
 prefill (pa_prefill), the int8 cache (pa_*_q8), the host block pool and
-prefix cache (BlockPool, PrefixCache), and the device pool with its beam step
-(DevicePool, pa_beam_step).
+prefix cache (BlockPool, PrefixCache), the device pool with its beam step
+(DevicePool, pa_beam_step) and its append and release (pa_dpool_append,
+pa_dpool_release), and the int8 cache with a scale per block (pa_*_q8b).
 
 Layouts (contiguous): k_cache/v_cache [num_blocks, num_kv_heads, block_size,
 head_dim]; query/out [num_seqs, num_heads, head_dim]; key/value
 [num_tokens, num_kv_heads, head_dim]; block_tables [num_seqs,
 max_blocks_per_seq] int32; context_lens [num_seqs] int32; slot_mapping
 [num_tokens] int32; src_dst_pairs [n, 2] int64; int8 caches add
-k_scale/v_scale [num_blocks, num_kv_heads, block_size] float32.
+k_scale/v_scale [num_blocks, num_kv_heads, block_size] float32, or
+[num_blocks, num_kv_heads] with a scale per block.
 """
 from __future__ import annotations
 
@@ -37,6 +39,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "libp
 PA_F32, PA_F16, PA_BF16 = 0, 1, 2
 _DT = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}
 
+PA_ERR_WORKSPACE = -9
 PA_DEVERR_BLOCK_ID = 0x1
 PA_DEVERR_SLOT = 0x2
 PA_DEVERR_CONTEXT = 0x4
@@ -45,6 +48,7 @@ PA_DEVERR_PAIR = 0x10
 PA_DEVERR_POOL = 0x20
 PA_DPOOL_HEADER_WORDS = 8
 PA_DPOOL_TAIL_WORDS = 1024
+PA_DPOOL_MAX_SEQS = 8192
 
 PA_POOL_LIFO, PA_POOL_FIFO = 0, 1
 
@@ -58,7 +62,8 @@ EXPORTED = (
     "pa_prefix_release", "pa_prefix_ref_count", "pa_copy_blocks_counted", "pa_dpool_state_bytes", "pa_dpool_init",
     "pa_beam_step", "pa_pool_export", "pa_dpool_load", "pa_reshape_and_cache_q8", "pa_decode_q8",
     "pa_decode_splitk_q8", "pa_copy_blocks_q8", "pa_decode_append", "pa_decode_withhold_stage",
-    "pa_prefill_withhold_tile", "pa_beam_step_withhold_arrival",
+    "pa_prefill_withhold_tile", "pa_beam_step_withhold_arrival", "pa_dpool_append", "pa_dpool_release",
+    "pa_append_q8b", "pa_decode_q8b", "pa_decode_q8b_workspace_bytes", "pa_copy_blocks_q8b",
 )
 
 PA_STATIC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -130,6 +135,13 @@ def _load() -> ctypes.CDLL:
         "pa_decode_splitk_q8": (i32, [vp, sz, vp, i32, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, f32, i32, i32,
                                       i32, i32, vp, vp]),
         "pa_copy_blocks_q8": (i32, [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp]),
+        "pa_dpool_append": (i32, [vp, i32, i32, vp, i32, vp, vp, i32, vp, vp, i32, vp, vp, vp]),
+        "pa_dpool_release": (i32, [vp, i32, i32, vp, i32, vp, vp, i32, vp]),
+        "pa_append_q8b": (i32, [vp, vp, i32, vp, i32, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, vp]),
+        "pa_decode_q8b_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
+        "pa_decode_q8b": (i32, [vp, vp, i32, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, f32, i32, i32, i32, i32,
+                                vp, vp, sz, vp]),
+        "pa_copy_blocks_q8b": (i32, [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -170,6 +182,12 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
     return t.data_ptr()
+
+
+def _expect(dtype: torch.dtype, *tensors: Optional[torch.Tensor]) -> None:
+    for t in tensors:
+        if t is not None and t.dtype != dtype:
+            raise ValueError(f"expected a {dtype} tensor, got {t.dtype}")
 
 
 def _stream(stream) -> Optional[int]:
@@ -441,6 +459,103 @@ def pa_beam_step_withhold_arrival(pool: DevicePool, old_tables, old_context_lens
         _ptr(slot_mapping) if num_new else None, _ptr(cow_pairs) if num_new else None, _ptr(num_cow), int(cta),
         int(wait_limit_ns), _stream(stream))
     _check(rc, "pa_beam_step_withhold_arrival")
+
+
+def pa_dpool_append(pool: DevicePool, block_tables, context_lens, new_lens, q_start, slot_mapping, cow_pairs, num_cow,
+                    stream=None) -> None:
+    """Sequence s appends new_lens[s] tokens: its blocks, table entries and
+    length in block_tables [S, MB] and context_lens [S], q_start [S + 1],
+    slots in slot_mapping [max_tokens] (then -1), pairs to copy in cow_pairs
+    [S, 2] int64 and their number in num_cow [1] (all on the device; see pa.h)."""
+    S = context_lens.shape[0]
+    if new_lens.shape[0] != S or block_tables.shape[0] != S or q_start.shape[0] != S + 1 or cow_pairs.shape[0] != S:
+        raise ValueError("pa_dpool_append: one row, length and pair per sequence, and one more q_start")
+    _expect(torch.int32, pool.state, block_tables, context_lens, new_lens, q_start, slot_mapping, num_cow)
+    _expect(torch.int64, cow_pairs)
+    T = slot_mapping.shape[0]
+    rc = _lib.pa_dpool_append(_ptr(pool.state), pool.num_blocks, pool.block_size, _ptr(block_tables) if S else None,
+                              block_tables.shape[1], _ptr(context_lens) if S else None, _ptr(new_lens) if S else None,
+                              S, _ptr(q_start), _ptr(slot_mapping) if T else None, T, _ptr(cow_pairs) if S else None,
+                              _ptr(num_cow), _stream(stream))
+    _check(rc, "pa_dpool_append")
+
+
+def pa_dpool_release(pool: DevicePool, block_tables, context_lens, finished, stream=None) -> None:
+    """Returns the blocks of every sequence s with finished[s] != 0 (device
+    int32 [S]); its table entries become -1 and its length 0."""
+    S = context_lens.shape[0]
+    if finished.shape[0] != S or block_tables.shape[0] != S:
+        raise ValueError("pa_dpool_release: one row, length and mark per sequence")
+    _expect(torch.int32, pool.state, block_tables, context_lens, finished)
+    rc = _lib.pa_dpool_release(_ptr(pool.state), pool.num_blocks, pool.block_size, _ptr(block_tables) if S else None,
+                               block_tables.shape[1], _ptr(context_lens) if S else None, _ptr(finished) if S else None,
+                               S, _stream(stream))
+    _check(rc, "pa_dpool_release")
+
+
+# ------------------------------------- int8 caches with a scale per block
+# k_cache/v_cache int8 [NB, Hkv, bs, D]; k_scale/v_scale float32 [NB, Hkv].
+
+def _q8b_cache(k_cache, v_cache, k_scale, v_scale):
+    _expect(torch.int8, k_cache, v_cache)
+    _expect(torch.float32, k_scale, v_scale)
+    if v_cache.shape != k_cache.shape or k_scale.shape != k_cache.shape[:2] or v_scale.shape != k_cache.shape[:2]:
+        raise ValueError("expected k_cache and v_cache [NB, Hkv, bs, D] with k_scale and v_scale [NB, Hkv]")
+    return k_cache.shape
+
+
+def pa_append_q8b(key, value, q_start, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                  stream=None) -> None:
+    """Writes rows q_start[s] .. q_start[s+1]-1 of key and value [T, Hkv, D] as
+    the last tokens of sequence s, quantized with one scale per (block, head)."""
+    NB, Hkv, bs, D = _q8b_cache(k_cache, v_cache, k_scale, v_scale)
+    S, T = context_lens.shape[0], key.shape[0]
+    if key.dtype != value.dtype or key.shape != (T, Hkv, D) or value.shape != key.shape:
+        raise ValueError("pa_append_q8b: key and value are [T, Hkv, D] of one type")
+    if q_start.shape[0] != S + 1 or block_tables.shape[0] != S:
+        raise ValueError("pa_append_q8b: one table row per sequence, and one more q_start")
+    _expect(torch.int32, q_start, block_tables, context_lens)
+    rc = _lib.pa_append_q8b(_ptr(key), _ptr(value), _dtype(key), _ptr(q_start), T, _ptr(k_cache), _ptr(v_cache),
+                            _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1],
+                            _ptr(context_lens), S, NB, Hkv, D, bs, _stream(stream))
+    _check(rc, "pa_append_q8b")
+
+
+def pa_decode_q8b_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len) -> int:
+    return int(_lib.pa_decode_q8b_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len))
+
+
+def pa_decode_q8b(out, query, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale, max_context_len,
+                  workspace=None, seq_order=None, stream=None) -> None:
+    """Decode over a cache with a scale per (block, head). max_context_len
+    bounds context_lens; with a workspace few, long sequences are split along
+    their tokens."""
+    NB, Hkv, bs, Dk = _q8b_cache(k_cache, v_cache, k_scale, v_scale)
+    S, Hq, D = query.shape
+    if Dk != D or out.shape != query.shape or context_lens.shape[0] != S or block_tables.shape[0] != S:
+        raise ValueError("pa_decode_q8b: query and out [S, Hq, D], one table row and length per sequence")
+    _expect(torch.int32, block_tables, context_lens, seq_order)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if workspace is not None and nbytes == 0:
+        _check(PA_ERR_WORKSPACE, "pa_decode_q8b")  # an empty tensor has no address: not "no workspace"
+    rc = _lib.pa_decode_q8b(_ptr(out), _ptr(query), _dtype(query), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                            _ptr(v_scale), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), S, Hq, Hkv,
+                            D, float(scale), bs, NB, int(max_context_len), _dtype(out), _ptr(seq_order),
+                            _ptr(workspace), nbytes, _stream(stream))
+    _check(rc, "pa_decode_q8b")
+
+
+def pa_copy_blocks_q8b(k_cache, v_cache, k_scale, v_scale, src_dst_pairs, num_pairs=None, stream=None) -> None:
+    """pa_copy_blocks of codes and scales; with num_pairs (a device int32) only
+    that many of the pairs."""
+    NB, Hkv, bs, D = _q8b_cache(k_cache, v_cache, k_scale, v_scale)
+    n = src_dst_pairs.shape[0] if src_dst_pairs is not None else 0
+    _expect(torch.int64, src_dst_pairs)
+    _expect(torch.int32, num_pairs)
+    rc = _lib.pa_copy_blocks_q8b(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                 _ptr(src_dst_pairs) if n else None, _ptr(num_pairs), n, NB, Hkv, D, bs,
+                                 _stream(stream))
+    _check(rc, "pa_copy_blocks_q8b")
 
 
 def pa_read_device_errors(stream=None) -> int:

@@ -33,33 +33,20 @@
 #include <algorithm>
 
 #include "pa_common.cuh"
+#include "pa_dpool.cuh"
 #include "pa_internal.h"
 
 namespace pa {
 namespace beam {
 
+using dpool::kMagic;
+using dpool::Pool;
+using dpool::views;
+
 constexpr int kThreads = 1024;     // pool set-up kernels
 // per-beam values staged in shared memory by each CTA of the step: 3 words
 // per old beam, 1 per new beam
 constexpr int kMaxStageBytes = PA_BEAM_MAX_STAGED * 4;
-constexpr int32_t kMagic = 0x50414250;
-
-struct Pool {
-    int32_t *hdr, *ref, *ring, *delta, *last_old, *writers, *last_writer, *tail;
-};
-
-__device__ __forceinline__ Pool views(int32_t *state, int nb) {
-    Pool p;
-    p.hdr = state;
-    p.ref = state + PA_DPOOL_HEADER_WORDS;
-    p.ring = p.ref + nb;
-    p.delta = p.ring + nb;
-    p.last_old = p.delta + nb;
-    p.writers = p.last_old + nb;
-    p.last_writer = p.writers + nb;
-    p.tail = p.last_writer + nb;
-    return p;
-}
 
 __global__ void __launch_bounds__(256) dpool_fill_kernel(int32_t *state, int nb, const int32_t *free_order) {
     const Pool p = views(state, nb);
