@@ -1,5 +1,41 @@
 // Paged decode attention over an int8 cache with one scale per (block, kv
-// head): out = softmax(scale q K^T) V with K_t = kq_t * k_scale[block, h].
+// head): out = softmax(scale q K^T) V with K_t = kq_t * k_scale[block, h],
+// V_t = vq_t * v_scale[block, h].
+//
+// The cache is read once and HBM bounds the call: an SM gets about 26 bytes a
+// clock of it, so the work per byte must stay off the warps. Both products run
+// on the 5th-generation tensor cores on the int8 codes as they lie in shared
+// memory; no code of the cache ever passes through a register.
+//   S^T = K Q^T   (M 128 = a tile's token rows, N = query columns, K = 128 bytes)
+//   O^T = V^T P^T (M 128 = head dims, N = probability columns, K = 128 tokens)
+// as tcgen05.mma kind::i8 with exact int32 sums. Query and probabilities enter
+// as fixed point in base 256, three columns a head:
+//   * q_d = qs * (65536 a + 256 b + c), signed digits, qs = max|q| / 8355711:
+//     23 bits of the head's largest element;
+//   * w_t = p_t v_scale_t / (the tile's largest one) = (65536 a + 256 b + c) /
+//     16777215, unsigned digits: 24 bits of the tile's largest weight. The
+//     block scales are folded in here, and the tile's largest weight is the
+//     unit, so a tile's sum is exact to 2^-17 of itself whatever the others
+//     hold; tiles are joined in fp32.
+// Scores, running maxima and sums are fp32 (log2 domain).
+//
+// One CTA per (sequence, kv head, up to 8 of its query heads[, partition]).
+// A tile is 128 rows of 128 bytes of K and of V. A row is one token at
+// head_dim 128 and two neighbouring tokens at 64: there each query head has two
+// columns ("virtual heads"), one for the even and one for the odd tokens, its
+// query padded with zeros over the other half, and the two are joined at the
+// end.
+//   * warps 5 and 6 load the K and the V tiles, one lane a block, through the
+//     table with 2-D TMA copies in the 128-byte swizzled layout, two stages each;
+//   * warp 4 issues the products: S_{j+2} as soon as S_j has been read, O_j when
+//     P_j has been written;
+//   * warps 0-3: thread r owns row r of S^T (a token row) and row r of O^T (a
+//     head dim). It forms the scores, keeps the running (max, sum) of its own
+//     tokens per head, agrees on the tile's largest weight with the other
+//     threads, writes the weights' digits, and adds up O_j in registers.
+// Rows past the sequence (or of a bad block) may hold anything: their weight is
+// 0, and 0 times an int8 code is 0.
+// Every wait is bounded (PA_DEVERR_TIMEOUT); tensor memory is always freed.
 #include <climits>
 #include <cmath>
 
@@ -11,9 +47,11 @@ namespace q8b {
 
 struct DecodeParams {
     void *out;
+    // split along the tokens: each partition's largest score m (log2 units), l = sum of 2^(score - m) and
+    // acc = sum of 2^(score - m) V
+    float *ws_ml;   // [num_seqs, num_heads, max_parts, 2]
+    float *ws_acc;  // [num_seqs, num_heads, max_parts, head_dim]
     const void *query;
-    const int8_t *k_cache;
-    const int8_t *v_cache;
     const float *k_scale;
     const float *v_scale;
     const int32_t *tables;
@@ -25,100 +63,632 @@ struct DecodeParams {
     int num_heads;
     int num_kv_heads;
     int group;
+    int sub_groups;
     int num_blocks;
-    int block_size;
+    int bs_shift;
+    int partition_size;  // tokens; 0: the whole sequence
+    int max_parts;
     float scale_log2;
     pa_dtype out_dtype;
     unsigned int *err;
 };
 
-constexpr int kWarps = 4;
-constexpr int kG = 8;  // query heads per CTA, at most
+constexpr int kG = 8;                          // query heads per CTA, at most
+constexpr int kRowBytes = 128;
+constexpr int kTile = 128 * kRowBytes;         // 16 KB of K or V
+constexpr int kStages = 2;
+constexpr int kSoftmaxThreads = 128;
+constexpr int kMmaWarp = 4, kLoadK = 5, kLoadV = 6;
+constexpr int kThreads = 7 * 32;
+constexpr int kQMax = 8355711;                 // 127 * 65536 + 127 * 256 + 127, three signed digits
+constexpr float kQUnit = 8355711.f;
+constexpr float kWUnit = 16777215.f;           // 2^24 - 1
 
-// One CTA per (sequence, kv head, up to 8 of its query heads); each warp takes
-// every fourth token, a lane D / 32 of its dims.
-template <typename T, int D> __global__ void __launch_bounds__(kWarps * 32) decode_kernel(const DecodeParams p) {
-    constexpr int kE = D / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int s = blockIdx.x;
+// V: virtual heads of the CTA (query heads, twice that at head_dim 64).
+template <int V> struct Shape {
+    static constexpr int kN = (3 * V + 15) / 16 * 16;  // MMA columns
+    static constexpr int kOffK = 0;
+    static constexpr int kOffV = kOffK + kStages * kTile;
+    static constexpr int kOffQ = kOffV + kStages * kTile;     // [kN][128] signed digits
+    static constexpr int kOffP = kOffQ + kN * kRowBytes;      // [kN][128] unsigned digits
+    static constexpr int kOffMax = kOffP + kN * kRowBytes;    // float [2][4 warps][V], tiles in turn
+    static constexpr int kOffQs = kOffMax + 8 * V * 4;        // float [V]: log2 score per unit of digits and k_scale
+    static constexpr int kOffBar = (kOffQs + V * 4 + 7) / 8 * 8;
+    static constexpr int kBars = 4 * kStages + 2 + 4;         // k/v full/empty, s_full[2], p_full, o_full, q_full, idle
+    static constexpr int kSmemBytes = 1024 + kOffBar + kBars * 8 + 16;
+    // tensor memory: S in two buffers, O in one
+    static constexpr int kSCol = 0, kOCol = 2 * kN;
+    static constexpr int kCols = 3 * kN <= 64 ? 64 : 3 * kN <= 128 ? 128 : 256;
+    // three CTAs an SM for up to 8 virtual heads, two for 16 (by shared memory as well as tensor memory)
+    static constexpr int kCtas = kCols <= 128 ? 3 : 2;
+    static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024 && (kCtas + 1) * (kSmemBytes + 1024) > 228 * 1024, "CTAs per SM");
+    static_assert(kCtas * kCols <= 512, "tensor memory");
+};
+
+// ------------------------------------------------------------- tensor cores
+
+// Shared-memory matrix descriptor, 128-byte swizzle, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc128(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Instruction descriptor of kind::i8, int32 sums, A signed, M 128.
+__host__ __device__ constexpr uint32_t idesc_i8(bool b_signed, bool a_mn_major, int N) {
+    return (2u << 4) | (1u << 7) | ((b_signed ? 1u : 0u) << 10) | ((a_mn_major ? 1u : 0u) << 15) |
+           ((uint32_t)(N >> 3) << 17) | (8u << 24);
+}
+
+__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// kC columns of this warp's 32 tensor-memory lanes (4, or a multiple of 4 by eights).
+template <int kC> __device__ __forceinline__ void tmem_load(uint32_t addr, int (&r)[kC]) {
+    static_assert(kC % 4 == 0, "columns");
+#pragma unroll
+    for (int i = 0; i + 8 <= kC; i += 8)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]),
+                       "=r"(r[i + 6]), "=r"(r[i + 7])
+                     : "r"(addr + i));
+    if constexpr (kC % 8 != 0)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[kC - 4]), "=r"(r[kC - 3]), "=r"(r[kC - 2]), "=r"(r[kC - 1])
+                     : "r"(addr + kC - 4));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    // the values exist from here on: no use of one may be moved above the wait
+#pragma unroll
+    for (int i = 0; i < kC; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Barrier over the softmax threads; true in all of them when `v` holds in all of them.
+__device__ __forceinline__ bool softmax_sync_and(bool v) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred pv, pa;\n\t"
+        "setp.ne.u32 pv, %1, 0;\n\t"
+        "barrier.cta.red.and.pred pa, 1, %2, pv;\n\t"
+        "selp.u32 %0, 1, 0, pa;\n\t}"
+        : "=r"(all)
+        : "r"((uint32_t)v), "n"(kSoftmaxThreads)
+        : "memory");
+    return all != 0;
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ------------------------------------------------------------------- kernel
+
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
+    decode_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                  const DecodeParams p) {
+    constexpr int kPar = 128 / D;   // tokens per row
+    constexpr int kV = G * kPar;    // virtual heads: par * G + g
+    using Sh = Shape<kV>;
+    constexpr int kN = Sh::kN;
+    constexpr int kCols3 = (3 * kV + 3) / 4 * 4;  // S columns read: three a virtual head
+    constexpr int kOCols3 = (3 * G + 3) / 4 * 4;  // O columns read: those of the lane's own tokens
+    constexpr int kTok = 128 * kPar;              // tokens per tile
+
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *sm =
+        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char *Qs = sm + Sh::kOffQ, *Ps = sm + Sh::kOffP;
+    float *wmax = reinterpret_cast<float *>(sm + Sh::kOffMax);
+    float *qscale = reinterpret_cast<float *>(sm + Sh::kOffQs);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Sh::kOffBar);
+    uint64_t *k_full = bars, *v_full = bars + kStages;              // a stage's tile has landed
+    uint64_t *k_empty = bars + 2 * kStages, *v_empty = bars + 3 * kStages;  // the product that read it is done
+    uint64_t *s_full = bars + 4 * kStages;                          // [2] S_j computed
+    uint64_t *p_full = s_full + 2;                                  // P_j written (and S_j, O_{j-1} read)
+    uint64_t *o_full = s_full + 3;                                  // O_j computed
+    uint64_t *q_full = s_full + 4;                                  // the query's digits are written
+    uint64_t *idle = s_full + 5;                                    // every product issued has finished
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Sh::kBars);
+    volatile int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int s = blockIdx.z;
     if (p.seq_order) {
         s = __ldg(p.seq_order + s);
         if (s < 0 || s >= p.num_seqs) {
-            if (threadIdx.x == 0) record_error(p.err, PA_DEVERR_CONTEXT);
+            if (tid == 0) record_error(p.err, PA_DEVERR_CONTEXT);
             return;
         }
     }
-    const int subs = (p.group + kG - 1) / kG;
-    const int kvh = blockIdx.y / subs, sub = blockIdx.y % subs;
-    const int head0 = kvh * p.group + sub * kG, g_valid = min(kG, p.group - sub * kG);
+    const int kvh = blockIdx.y / p.sub_groups, sub = blockIdx.y % p.sub_groups;
+    const int head0 = kvh * p.group + sub * kG, g_valid = min(G, p.group - sub * kG);
     int L = __ldg(p.ctx + s);
-    const long long room = min((long long)p.max_blocks * p.block_size, (long long)p.max_ctx);
+    const int room = (int)min((long long)p.max_blocks << p.bs_shift, (long long)p.max_ctx);
     if (L < 0 || L > room) {
-        if (threadIdx.x == 0) record_error(p.err, PA_DEVERR_CONTEXT);
-        L = L < 0 ? 0 : (int)room;
+        if (tid == 0) record_error(p.err, PA_DEVERR_CONTEXT);
+        L = L < 0 ? 0 : room;
     }
-    float q[kG][kE], o[kG][kE], m[kG], l[kG];
-#pragma unroll
-    for (int g = 0; g < kG; ++g) {
-        m[g] = -INFINITY;
-        l[g] = 0.f;
-#pragma unroll
-        for (int e = 0; e < kE; ++e) {
-            q[g][e] = g < g_valid ? (float)static_cast<const T *>(p.query)[((size_t)s * p.num_heads + head0 + g) * D +
-                                                                           lane * kE + e] * p.scale_log2
-                                  : 0.f;
-            o[g][e] = 0.f;
-        }
+    // this CTA's tokens: first .. L - 1, tiles of kTok
+    const int first = blockIdx.x * p.partition_size;
+    if (p.partition_size) {
+        L = min(L, first + p.partition_size);
+        if (first >= L) return;  // no such partition: its entry is not read
     }
-    for (int t = warp; t < L; t += kWarps) {
-        const int id = __ldg(p.tables + (size_t)s * p.max_blocks + t / p.block_size);
-        if (id < 0 || id >= p.num_blocks) {
-            if (lane == 0) record_error(p.err, PA_DEVERR_BLOCK_ID);
-            continue;
-        }
-        const size_t unit = (size_t)id * p.num_kv_heads + kvh;
-        const size_t at = (unit * p.block_size + t % p.block_size) * D + lane * kE;
-        const float ks = __ldg(p.k_scale + unit), vs = __ldg(p.v_scale + unit);
-#pragma unroll
-        for (int g = 0; g < kG; ++g) {
-            float x = 0.f;
-#pragma unroll
-            for (int e = 0; e < kE; ++e) x = fmaf(q[g][e], (float)p.k_cache[at + e], x);
-#pragma unroll
-            for (int mk = 16; mk >= 1; mk >>= 1) x += __shfl_xor_sync(0xffffffffu, x, mk);
-            x *= ks;
-            const float mn = fmaxf(m[g], x);
-            const float a = fast_exp2(m[g] - mn), w = fast_exp2(x - mn);
-            m[g] = mn;
-            l[g] = l[g] * a + w;
-#pragma unroll
-            for (int e = 0; e < kE; ++e) o[g][e] = fmaf(o[g][e], a, w * vs * (float)p.v_cache[at + e]);
-        }
+    const size_t row0 = (size_t)s * p.num_heads + head0;  // output row of head 0
+    if (L <= 0) {
+        for (int i = tid; i < g_valid * D; i += kThreads) store_out(p.out, row0 * D + i, 0.f, p.out_dtype);
+        return;
     }
-    __shared__ float sm[kWarps][kG], sl[kWarps][kG], so[kWarps][kG][D];
-#pragma unroll
-    for (int g = 0; g < kG; ++g) {
-        if (lane == 0) {
-            sm[warp][g] = m[g];
-            sl[warp][g] = l[g];
-        }
-#pragma unroll
-        for (int e = 0; e < kE; ++e) so[warp][g][lane * kE + e] = o[g][e];
+    const int ntiles = (L - first + kTok - 1) / kTok;
+    const int32_t *trow = p.tables + (size_t)s * p.max_blocks;
+    const int bs_shift = p.bs_shift;
+
+    if (tid == 0) {
+        for (int i = 0; i < 4 * kStages; ++i) mbar_init(bars + i, 1);
+        mbar_init(s_full, 1);
+        mbar_init(s_full + 1, 1);
+        mbar_init(p_full, kSoftmaxThreads);
+        mbar_init(o_full, 1);
+        mbar_init(q_full, kSoftmaxThreads);
+        mbar_init(idle, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        fence_proxy_async_smem();
     }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
+                     "r"(Sh::kCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // digit columns past the heads, and padding heads, stay zero
+    for (int i = tid; i < 2 * kN * kRowBytes / 16; i += kThreads)
+        reinterpret_cast<uint4 *>(Qs)[i] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();  // each thread's zeros, before the products read them
+    fence_before();
     __syncthreads();
-    for (int i = threadIdx.x; i < g_valid * D; i += kWarps * 32) {
-        const int g = i / D, d = i % D;
-        float M = -INFINITY;
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w][g]);
-        float num = 0.f, den = 0.f;
-        if (M > -INFINITY)
-            for (int w = 0; w < kWarps; ++w) {
-                const float a = fast_exp2(sm[w][g] - M);
-                num = fmaf(a, so[w][g][d], num);
-                den = fmaf(a, sl[w][g], den);
+    fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp >= kLoadK) {
+        // ====================================================== load warps
+        // Lane i brings block i of the tile: kBoxRows rows of 128 bytes.
+        const bool is_v = warp == kLoadV;
+        const CUtensorMap *map = is_v ? &v_map : &k_map;
+        uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
+        unsigned char *ring = sm + (is_v ? Sh::kOffV : Sh::kOffK);
+        const int blocks = kTok >> bs_shift;         // per tile: 4, 8 or 16
+        const int rows = 128 / blocks;               // 128-byte rows of a block
+        const int b0 = first >> bs_shift, nblk = (L + (1 << bs_shift) - 1) >> bs_shift;
+        auto look = [&](int j) -> int {
+            const int lb = b0 + j * blocks + lane;
+            return (lane < blocks && lb < nblk) ? __ldg(trow + lb) : -1;
+        };
+        int id = look(0), id_next = look(1);
+        int issued = 0;
+        for (int j = 0; j < ntiles; ++j) {
+            const int b = j % kStages;
+            if (j >= kStages) {
+                const bool got = mbar_wait(empty + b, (j / kStages - 1) & 1) && !*abort_flag;
+                if (!__all_sync(0xffffffffu, got)) {
+                    if (lane == 0) {
+                        record_error(p.err, PA_DEVERR_TIMEOUT);
+                        *abort_flag = 1;
+                    }
+                    break;
+                }
             }
-        store_out(p.out, ((size_t)s * p.num_heads + head0 + g) * D + d, den > 0.f ? num / den : 0.f, p.out_dtype);
+            const bool here = lane < blocks && b0 + j * blocks + lane < nblk;
+            const bool ok = here && id >= 0 && id < p.num_blocks;
+            if (here && !ok) record_error(p.err, PA_DEVERR_BLOCK_ID);
+            const unsigned m = __ballot_sync(0xffffffffu, ok);
+            if (lane == 0) mbar_arrive_expect_tx(full + b, __popc(m) * rows * kRowBytes);
+            __syncwarp();
+            if (ok)
+                tma_load_2d(ring + b * kTile + lane * rows * kRowBytes, map, 0, (id * p.num_kv_heads + kvh) * rows,
+                            full + b);
+            ++issued;
+            id = id_next;
+            id_next = look(j + 2);
+        }
+        // copies in flight land before the CTA leaves
+        for (int j = max(0, issued - kStages); j < issued; ++j) mbar_wait(full + j % kStages, (j / kStages) & 1);
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ======================================================== MMA warp
+        if (lane == 0) {
+            constexpr uint32_t kIdQK = idesc_i8(true, false, kN), kIdPV = idesc_i8(false, true, kN);
+            const uint32_t qa = smem_addr(Qs), pa_ = smem_addr(Ps);
+            bool ok = mbar_wait(q_full, 0) && !*abort_flag;
+            auto issue_s = [&](int j) -> bool {
+                const int b = j % kStages;
+                if (!mbar_wait(k_full + b, (j / kStages) & 1) || *abort_flag) return false;
+                fence_after();
+                const uint32_t ka = smem_addr(sm + Sh::kOffK) + b * kTile;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_i8(tmem + Sh::kSCol + (j & 1) * kN, desc128(ka + kk * 32), desc128(qa + kk * 32), kIdQK, kk > 0);
+                mma_commit(s_full + (j & 1));
+                mma_commit(k_empty + b);
+                return true;
+            };
+            for (int j = 0; ok && j < min(2, ntiles); ++j) ok = issue_s(j);
+            for (int j = 0; ok && j < ntiles; ++j) {
+                const int b = j % kStages;
+                if (!mbar_wait(p_full, j & 1) || !mbar_wait(v_full + b, (j / kStages) & 1) || *abort_flag) {
+                    ok = false;
+                    break;
+                }
+                fence_after();
+                const uint32_t va = smem_addr(sm + Sh::kOffV) + b * kTile;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_i8(tmem + Sh::kOCol, desc128(va + kk * 32 * kRowBytes), desc128(pa_ + kk * 32), kIdPV, kk > 0);
+                mma_commit(o_full);
+                mma_commit(v_empty + b);
+                if (j + 2 < ntiles) ok = issue_s(j + 2);
+            }
+            if (!ok) {
+                record_error(p.err, PA_DEVERR_TIMEOUT);
+                *abort_flag = 1;
+            }
+            // tensor memory is freed below: every product issued must have finished
+            mma_commit(idle);
+            if (!mbar_wait(idle, 0)) record_error(p.err, PA_DEVERR_TIMEOUT);
+        }
+        __syncwarp();
+    } else {
+        // =================================================== softmax warps
+        const int r = tid;
+        const uint32_t tlane = tmem + ((uint32_t)(warp * 32) << 16);
+        // ---- the query's digits: warp w takes heads w, w + 4
+#pragma unroll
+        for (int g0 = 0; g0 < G; g0 += 4) {
+            const int g = g0 + warp;
+            if (g < G) {
+                constexpr int kE = D / 32;
+                float x[kE];
+                float amax = 0.f, odd = 0.f;  // odd: NaN if an element is not finite
+#pragma unroll
+                for (int e = 0; e < kE; ++e) {
+                    x[e] = g < g_valid ? (float)static_cast<const T *>(p.query)[(row0 + g) * D + lane * kE + e] : 0.f;
+                    amax = fmaxf(amax, fabsf(x[e]));
+                    odd += x[e] * 0.f;
+                }
+                amax = warp_max(amax);
+#pragma unroll
+                for (int mk = 16; mk >= 1; mk >>= 1) odd += __shfl_xor_sync(0xffffffffu, odd, mk);
+                // a query below 2^-100 counts as zero (its unit's reciprocal would not be finite)
+                const bool live = amax >= 7.888609e-31f && odd == 0.f;
+                const float inv = live ? kQUnit / amax : 0.f;
+#pragma unroll
+                for (int e = 0; e < kE; ++e) {
+                    // (the product may round up past the unit)
+                    const int q = live ? max(-kQMax, min(kQMax, __float2int_rn(x[e] * inv))) : 0;
+                    const int c = (int)(int8_t)q, q1 = (q - c) >> 8;
+                    const int b = (int)(int8_t)q1, a = (q1 - b) >> 8;
+#pragma unroll
+                    for (int par = 0; par < kPar; ++par) {
+                        const int n = (par * G + g) * 3, at = par * D + lane * kE + e;
+                        Qs[n * kRowBytes + (at ^ ((n & 7) << 4))] = (unsigned char)a;
+                        Qs[(n + 1) * kRowBytes + (at ^ (((n + 1) & 7) << 4))] = (unsigned char)b;
+                        Qs[(n + 2) * kRowBytes + (at ^ (((n + 2) & 7) << 4))] = (unsigned char)c;
+                    }
+                }
+                if (lane < kPar) qscale[lane * G + g] = (live ? amax / kQUnit : 0.f) * p.scale_log2 + odd;
+            }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(q_full);
+        named_bar_sync(1, kSoftmaxThreads);
+        float qs[kV];
+#pragma unroll
+        for (int v = 0; v < kV; ++v) qs[v] = qscale[v];
+
+        // ---- tiles. The scales of row r's block come two tiles ahead (its id) and one tile ahead.
+        const int nblk = (L + (1 << bs_shift) - 1) >> bs_shift;
+        auto look = [&](int j) -> int {
+            const int lb = (first + j * kTok + r * kPar) >> bs_shift;
+            const int id = (j < ntiles && lb < nblk) ? __ldg(trow + lb) : -1;
+            return id < p.num_blocks ? id : -1;
+        };
+        float ks = 0.f, vs = 0.f;
+        int id = look(0), id_next = look(1);
+        if (id >= 0) {
+            ks = __ldg(p.k_scale + (size_t)id * p.num_kv_heads + kvh);
+            vs = __ldg(p.v_scale + (size_t)id * p.num_kv_heads + kvh);
+        }
+        float m_l[kV], l[kV];            // this thread's tokens: largest score, sum of 2^(score - it)
+        float m_o[G], o[G], m_tile[G];   // O of the lane's dim: sum * 2^-m_o; the unit of the tile in tensor memory
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            m_l[v] = -INFINITY;
+            l[v] = 0.f;
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            m_o[g] = m_tile[g] = -INFINITY;
+            o[g] = 0.f;
+        }
+        const int par0 = kPar == 2 ? (warp >> 1) * G : 0;  // first virtual head of this lane's tokens
+        // adds the tile in tensor memory (its O columns, in units of 2^m_tile / kWUnit) to o
+        auto add_tile = [&]() {
+            int t[kOCols3];
+            tmem_load<kOCols3>(tlane + Sh::kOCol + 3 * par0, t);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const float f = fmaf((float)t[3 * g], 65536.f, (float)(t[3 * g + 1] * 256 + t[3 * g + 2]));
+                if (m_tile[g] > m_o[g]) {  // the same in every thread of the warp
+                    o[g] = o[g] * fast_exp2(m_o[g] - m_tile[g]) + f;
+                    m_o[g] = m_tile[g];
+                } else if (m_tile[g] > -INFINITY) {
+                    o[g] = fmaf(f, fast_exp2(m_tile[g] - m_o[g]), o[g]);
+                }
+            }
+        };
+        // The four warps leave the loop together: one whose wait ran out says so
+        // at the tile's barrier.
+        bool sound = true, ok = true;
+        for (int j = 0; j < ntiles; ++j) {
+            // the next tile's scales
+            float ks_next = 0.f, vs_next = 0.f;
+            if (id_next >= 0) {
+                ks_next = __ldg(p.k_scale + (size_t)id_next * p.num_kv_heads + kvh);
+                vs_next = __ldg(p.v_scale + (size_t)id_next * p.num_kv_heads + kvh);
+            }
+            const int id_after = look(j + 2);
+            const float lv = vs > 0.f ? log2f(vs) : -INFINITY;
+            const int tok = first + j * kTok + r * kPar;
+            float *wm = wmax + (j & 1) * 4 * kV;
+
+            sound = __all_sync(0xffffffffu, sound && mbar_wait(s_full + (j & 1), (j >> 1) & 1) && !*abort_flag);
+            float x[kV];  // log2 of the weight
+            if (sound) {
+                fence_after();
+                int t[kCols3];
+                tmem_load<kCols3>(tlane + Sh::kSCol + (j & 1) * kN, t);
+#pragma unroll
+                for (int v = 0; v < kV; ++v) {
+                    const float f = fmaf((float)t[3 * v], 65536.f, (float)(t[3 * v + 1] * 256 + t[3 * v + 2]));
+                    const float sc = f * (qs[v] * ks);
+                    const bool live = id >= 0 && tok + v / G < L;
+                    if (live) {
+                        const float d = sc - m_l[v];
+                        const float e = fast_exp2(-fabsf(d));
+                        l[v] = d > 0.f ? fmaf(l[v], e, 1.f) : l[v] + e;
+                        m_l[v] = fmaxf(m_l[v], sc);
+                    }
+                    x[v] = live ? sc + lv : -INFINITY;
+                }
+                // the tile's largest weight per head, over this warp
+#pragma unroll
+                for (int v = 0; v < kV; ++v) {
+                    const float mw = warp_max(x[v]);
+                    if (lane == 0) wm[warp * kV + v] = mw;
+                }
+            }
+            ok = softmax_sync_and(sound);
+            if (!ok) break;
+            float mt[kV];
+#pragma unroll
+            for (int v = 0; v < kV; ++v)
+                mt[v] = fmaxf(fmaxf(wm[v], wm[kV + v]), fmaxf(wm[2 * kV + v], wm[3 * kV + v]));
+            if (j > 0) {  // O_{j-1} is there: P and O are free once it is added up
+                sound = __all_sync(0xffffffffu, mbar_wait(o_full, (j - 1) & 1) && !*abort_flag);
+                if (!sound) continue;  // (the next tile's barrier, or the one behind the loop, tells the others)
+                fence_after();
+                add_tile();
+            }
+#pragma unroll
+            for (int g = 0; g < G; ++g) m_tile[g] = kPar == 2 && par0 ? mt[kV - G + g] : mt[g];
+            // ---- the weights' digits, column 3 v + i, byte r of the row (its 16-byte chunk swizzled)
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                const float w = x[v] > -INFINITY ? fast_exp2(x[v] - mt[v]) : 0.f;
+                const unsigned u = __float2uint_rn(w * kWUnit);
+                const int n = 3 * v;
+                Ps[n * kRowBytes + (r ^ ((n & 7) << 4))] = (unsigned char)(u >> 16);
+                Ps[(n + 1) * kRowBytes + (r ^ (((n + 1) & 7) << 4))] = (unsigned char)(u >> 8);
+                Ps[(n + 2) * kRowBytes + (r ^ (((n + 2) & 7) << 4))] = (unsigned char)u;
+            }
+            fence_proxy_async_smem();
+            fence_before();
+            mbar_arrive(p_full);
+            id = id_next;
+            id_next = id_after;
+            ks = ks_next;
+            vs = vs_next;
+        }
+        if (ok) {
+            sound = __all_sync(0xffffffffu, sound && mbar_wait(o_full, (ntiles - 1) & 1) && !*abort_flag);
+            if (sound) {
+                fence_after();
+                add_tile();
+            }
+            ok = softmax_sync_and(sound);
+        }
+        // ---- the threads' sums, and the output. Every product is done (o_full),
+        // so the K tiles are free to hold them.
+        float *red_m = reinterpret_cast<float *>(sm), *red_l = red_m + 4 * kV;
+        float *red_o = red_l + 4 * kV;  // [G][64]: the odd tokens' sums at head_dim 64
+        if (!ok) {
+            if (r == 0) record_error(p.err, PA_DEVERR_TIMEOUT);
+        } else {
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                const float mw = warp_max(m_l[v]);
+                float lw = m_l[v] > -INFINITY ? l[v] * fast_exp2(m_l[v] - mw) : l[v];
+#pragma unroll
+                for (int mk = 16; mk >= 1; mk >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, mk);
+                if (lane == 0) {
+                    red_m[warp * kV + v] = mw;
+                    red_l[warp * kV + v] = lw;
+                }
+            }
+            named_bar_sync(1, kSoftmaxThreads);
+            float m[G], sum[G];
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                m[g] = -INFINITY;
+                sum[g] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4 * kPar; ++i) m[g] = fmaxf(m[g], red_m[(i & 3) * kV + (i >> 2) * G + g]);
+#pragma unroll
+                for (int i = 0; i < 4 * kPar; ++i) {
+                    const float mi = red_m[(i & 3) * kV + (i >> 2) * G + g], li = red_l[(i & 3) * kV + (i >> 2) * G + g];
+                    sum[g] += mi > -INFINITY ? li * fast_exp2(mi - m[g]) : li;  // a NaN query's sum is NaN
+                }
+                o[g] = m_o[g] > -INFINITY ? o[g] * fast_exp2(m_o[g] - m[g]) : 0.f;
+                if (kPar == 2 && r >= D) red_o[g * D + r - D] = o[g];
+            }
+            if constexpr (kPar == 2) named_bar_sync(1, kSoftmaxThreads);
+            if (r < D) {
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    if (g >= g_valid) continue;
+                    if constexpr (kPar == 2) o[g] += red_o[g * D + r];
+                    const size_t row = row0 + g;
+                    if (p.partition_size) {
+                        const size_t slot = row * p.max_parts + blockIdx.x;
+                        p.ws_acc[slot * D + r] = o[g] * (1.f / kWUnit);
+                        if (r == 0) {
+                            p.ws_ml[slot * 2] = m[g];  // log2 units
+                            p.ws_ml[slot * 2 + 1] = sum[g];
+                        }
+                    } else {
+                        const float y = sum[g] != 0.f ? o[g] / (sum[g] * kWUnit) : 0.f;
+                        store_out(p.out, row * D + r, y, p.out_dtype);
+                    }
+                }
+            }
+        }
     }
+    fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Sh::kCols) : "memory");
+    }
+}
+
+// Joins the partitions: out = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) l_p.
+// One CTA per (head, sequence); warp w takes partitions w, w + 4, .., a lane
+// D / 32 dims, and the warps are joined in shared memory.
+template <int D> __global__ void __launch_bounds__(128) join_kernel(const DecodeParams p) {
+    constexpr int kE = D / 32, kU = 4;
+    __shared__ float sm_m[4], sm_l[4], sm_o[4][D];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int s = blockIdx.y;
+    if (p.seq_order) {
+        s = __ldg(p.seq_order + s);
+        if (s < 0 || s >= p.num_seqs) return;  // recorded by decode_kernel
+    }
+    const long long room = min((long long)p.max_blocks << p.bs_shift, (long long)p.max_ctx);
+    const int L = (int)min((long long)max(__ldg(p.ctx + s), 0), room);
+    const int n = (L + p.partition_size - 1) / p.partition_size;
+    const size_t row = (size_t)s * p.num_heads + blockIdx.x;
+    const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml) + row * p.max_parts;
+    const float *acc = p.ws_acc + row * p.max_parts * D + lane * kE;
+    float m = -INFINITY, l = 0.f, o[kE] = {};
+    for (int i0 = warp; i0 < n; i0 += 4 * kU) {
+        float2 v[kU];
+        float a[kU][kE];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {  // kU partitions' loads in flight
+            const int i = i0 + 4 * u;
+            v[u] = i < n ? ml[i] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int e = 0; e < kE; ++e) a[u][e] = i < n ? acc[(size_t)i * D + e] : 0.f;
+        }
+        float mn = m;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) mn = fmaxf(mn, v[u].x);
+        const float r = m > -INFINITY ? fast_exp2(m - mn) : 0.f;
+        l *= r;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) o[e] *= r;
+        m = mn;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const float w = v[u].x > -INFINITY ? fast_exp2(v[u].x - m) : 0.f;
+            l += v[u].x > -INFINITY ? w * v[u].y : v[u].y;  // (a NaN sum stays)
+#pragma unroll
+            for (int e = 0; e < kE; ++e) o[e] = fmaf(w, a[u][e], o[e]);
+        }
+    }
+    if (lane == 0) {
+        sm_m[warp] = m;
+        sm_l[warp] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < kE; ++e) sm_o[warp][lane * kE + e] = o[e];
+    __syncthreads();
+    const int d = threadIdx.x;
+    if (d >= D) return;
+    const float M = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
+    float num = 0.f, den = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float f = sm_m[w] > -INFINITY ? fast_exp2(sm_m[w] - M) : 0.f;
+        num = fmaf(f, sm_o[w][d], num);
+        den += sm_m[w] > -INFINITY ? f * sm_l[w] : sm_l[w];
+    }
+    store_out(p.out, row * D + d, den != 0.f ? num / den : 0.f, p.out_dtype);
+}
+
+template <typename T, int D, int G>
+static cudaError_t launch_decode_t(const CUtensorMap &km, const CUtensorMap &vm, const DecodeParams &p,
+                                   cudaStream_t stream) {
+    auto kern = decode_kernel<T, D, G>;
+    constexpr int kSmem = Shape<G * (128 / D)>::kSmemBytes;
+    static AttrCache attr;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmem, &attr);
+    if (e != cudaSuccess) return e;
+    kern<<<dim3(p.max_parts, p.num_kv_heads * p.sub_groups, p.num_seqs), kThreads, kSmem, stream>>>(km, vm, p);
+    return cudaGetLastError();
+}
+
+template <typename T>
+static cudaError_t launch_decode(const CUtensorMap &km, const CUtensorMap &vm, const DecodeParams &p, int head_dim,
+                                 cudaStream_t stream) {
+    const int g = p.group;  // rounded up to a power of two, at most kG
+#define PA_Q8B(DD) \
+    (g == 1 ? launch_decode_t<T, DD, 1>(km, vm, p, stream) : g == 2 ? launch_decode_t<T, DD, 2>(km, vm, p, stream) \
+     : g <= 4 ? launch_decode_t<T, DD, 4>(km, vm, p, stream) : launch_decode_t<T, DD, 8>(km, vm, p, stream))
+    return head_dim == 128 ? PA_Q8B(128) : PA_Q8B(64);
+#undef PA_Q8B
+}
+
+// Tokens of a partition: 0 where the (sequence, kv head) pairs alone give the
+// GPU enough CTAs, or a sequence is one tile.
+static int partition_of(int num_seqs, int rows_y, int head_dim, int max_ctx) {
+    const int tok = 128 * (128 / head_dim);
+    const long long items = (long long)num_seqs * rows_y, tiles = ((long long)max_ctx + tok - 1) / tok;
+    const long long target = 6ll * sm_count();
+    if (items >= target / 2 || tiles < 2) return 0;
+    long long parts = (target + items - 1) / items;
+    if (parts > tiles) parts = tiles;
+    const long long per = (tiles + parts - 1) / parts;
+    return per >= tiles ? 0 : (int)(per * tok);
+}
+
+// CTAs along the kv heads: a group above kG query heads takes several.
+static long long rows_of(int num_heads, int num_kv_heads) {
+    return (long long)num_kv_heads * ((num_heads / num_kv_heads + kG - 1) / kG);
 }
 
 static bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -130,8 +700,14 @@ using namespace pa;
 
 extern "C" size_t pa_decode_q8b_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                                                 int max_context_len) {
-    if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || max_context_len < 0) return 0;
-    return 16;
+    if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 ||
+        (head_dim != 64 && head_dim != 128) || max_context_len < 0 || num_heads % num_kv_heads != 0 ||
+        q8b::rows_of(num_heads, num_kv_heads) > 65535)
+        return 0;
+    const int rows_y = (int)q8b::rows_of(num_heads, num_kv_heads);
+    const int P = q8b::partition_of(num_seqs, rows_y, head_dim, max_context_len);
+    // at least 16 bytes, so that a workspace of the size asked for is always one
+    return P ? pa_splitk_workspace_bytes(num_seqs, num_heads, head_dim, max_context_len, P) : 16;
 }
 
 extern "C" int pa_decode_q8b(void *out, const void *query, pa_dtype q_dtype, const int8_t *k_cache,
@@ -149,7 +725,7 @@ extern "C" int pa_decode_q8b(void *out, const void *query, pa_dtype q_dtype, con
     if (block_size != 16 && block_size != 32) return PA_ERR_BLOCK_SIZE;
     if (num_heads % num_kv_heads != 0) return PA_ERR_HEADS;
     const int group = num_heads / num_kv_heads;
-    const long long rows_y = (long long)num_kv_heads * ((group + q8b::kG - 1) / q8b::kG);
+    const long long rows_y = q8b::rows_of(num_heads, num_kv_heads);
     if (rows_y > 65535 || max_blocks_per_seq > INT_MAX / block_size ||
         (long long)num_blocks * num_kv_heads * block_size >= INT_MAX)
         return PA_ERR_SHAPE;
@@ -168,8 +744,6 @@ extern "C" int pa_decode_q8b(void *out, const void *query, pa_dtype q_dtype, con
     if (device_error_word(&p.err) != cudaSuccess) return PA_ERR_CUDA;
     p.out = out;
     p.query = query;
-    p.k_cache = k_cache;
-    p.v_cache = v_cache;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
     p.tables = block_tables;
@@ -182,16 +756,35 @@ extern "C" int pa_decode_q8b(void *out, const void *query, pa_dtype q_dtype, con
     p.num_kv_heads = num_kv_heads;
     p.group = group;
     p.num_blocks = num_blocks;
-    p.block_size = block_size;
+    p.sub_groups = (int)(rows_y / num_kv_heads);
+    p.bs_shift = block_size == 16 ? 4 : 5;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.out_dtype = out_dtype;
-    const dim3 grid((unsigned)num_seqs, (unsigned)rows_y);
-    if (q_dtype == PA_F16) {
-        if (head_dim == 128) q8b::decode_kernel<__half, 128><<<grid, q8b::kWarps * 32, 0, stream>>>(p);
-        else q8b::decode_kernel<__half, 64><<<grid, q8b::kWarps * 32, 0, stream>>>(p);
-    } else {
-        if (head_dim == 128) q8b::decode_kernel<__nv_bfloat16, 128><<<grid, q8b::kWarps * 32, 0, stream>>>(p);
-        else q8b::decode_kernel<__nv_bfloat16, 64><<<grid, q8b::kWarps * 32, 0, stream>>>(p);
+    p.max_parts = 1;
+    const int P = workspace ? q8b::partition_of(num_seqs, (int)rows_y, head_dim, max_context_len) : 0;
+    if (P) {
+        p.partition_size = P;
+        p.max_parts = (max_context_len + P - 1) / P;
+        p.ws_ml = static_cast<float *>(workspace);
+        p.ws_acc = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) +
+                                             pa_splitk_acc_offset(num_seqs, num_heads, max_context_len, P));
     }
-    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    // the pools as rows of 128 bytes, a block at a time
+    const unsigned box = (unsigned)(block_size * head_dim / 128);
+    const unsigned long long rows = (unsigned long long)num_blocks * num_kv_heads * box;
+    CUtensorMap km, vm;
+    if (!encode_rows_2d(&km, CU_TENSOR_MAP_DATA_TYPE_UINT8, k_cache, 128, rows ? rows : 1, 128, 128, box,
+                        CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_rows_2d(&vm, CU_TENSOR_MAP_DATA_TYPE_UINT8, v_cache, 128, rows ? rows : 1, 128, 128, box,
+                        CU_TENSOR_MAP_SWIZZLE_128B))
+        return PA_ERR_CUDA;
+    cudaError_t e = q_dtype == PA_F16 ? q8b::launch_decode<__half>(km, vm, p, head_dim, stream)
+                                      : q8b::launch_decode<__nv_bfloat16>(km, vm, p, head_dim, stream);
+    if (e == cudaSuccess && P) {
+        const dim3 grid((unsigned)num_heads, (unsigned)num_seqs);
+        if (head_dim == 128) q8b::join_kernel<128><<<grid, 128, 0, stream>>>(p);
+        else q8b::join_kernel<64><<<grid, 128, 0, stream>>>(p);
+        e = cudaGetLastError();
+    }
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
