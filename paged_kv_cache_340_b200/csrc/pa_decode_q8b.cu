@@ -19,25 +19,35 @@
 //     hold; tiles are joined in fp32.
 // Scores, running maxima and sums are fp32 (log2 domain).
 //
-// One CTA per (sequence, kv head, up to 8 of its query heads[, partition]).
+// A work item is a (sequence, kv head, up to 8 of its query heads[,
+// partition]); the grid has one block per item. A resident CTA takes over
+// blocks that have not started yet (clusterlaunchcontrol.try_cancel), one ahead
+// of the item it works on, so K and V tiles of the next item stream in while the
+// last one ends: a CTA per item lost about 3 us to each item's first lookups.
 // A tile is 128 rows of 128 bytes of K and of V. A row is one token at
 // head_dim 128 and two neighbouring tokens at 64: there each query head has two
 // columns ("virtual heads"), one for the even and one for the odd tokens, its
 // query padded with zeros over the other half, and the two are joined at the
 // end.
+//   * warp 7 claims the items, looks up what the other warps need of them and
+//     writes the query's digits, two items deep;
 //   * warps 5 and 6 load the K and the V tiles, one lane a block, through the
-//     table with 2-D TMA copies in the 128-byte swizzled layout, two stages each;
-//   * warp 4 issues the products: S_{j+2} as soon as S_j has been read, O_j when
-//     P_j has been written;
+//     table with 2-D TMA copies in the 128-byte swizzled layout, two stages
+//     each; warp 5 also puts the tile's block scales beside them;
+//   * warp 4 issues the products: S of tile t + 2 as soon as S of tile t has
+//     been read, O of tile t when its weights have been written;
 //   * warps 0-3: thread r owns row r of S^T (a token row) and row r of O^T (a
 //     head dim). It forms the scores, keeps the running (max, sum) of its own
 //     tokens per head, agrees on the tile's largest weight with the other
-//     threads, writes the weights' digits, and adds up O_j in registers.
+//     threads, writes the weights' digits, and adds up O in registers (which it
+//     takes over from the other four warps: setmaxnreg).
 // Rows past the sequence (or of a bad block) may hold anything: their weight is
 // 0, and 0 times an int8 code is 0.
 // Every wait is bounded (PA_DEVERR_TIMEOUT); tensor memory is always freed.
+#include <atomic>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "pa_common.cuh"
 #include "pa_internal.h"
@@ -68,41 +78,77 @@ struct DecodeParams {
     int bs_shift;
     int partition_size;  // tokens; 0: the whole sequence
     int max_parts;
+    int steal;  // whether a CTA takes over further blocks of the grid
     float scale_log2;
     pa_dtype out_dtype;
     unsigned int *err;
 };
 
-constexpr int kG = 8;                          // query heads per CTA, at most
+constexpr int kG = 8;                          // query heads per item, at most
 constexpr int kRowBytes = 128;
 constexpr int kTile = 128 * kRowBytes;         // 16 KB of K or V
 constexpr int kStages = 2;
+constexpr int kItems = 2;                      // items known ahead, the current one included
+constexpr int kScales = 4;                     // tiles whose scales are kept: warp 5 is at most three tiles ahead
+constexpr int kMaxBlocks = 16;                 // blocks of a tile, at most
 constexpr int kSoftmaxThreads = 128;
-constexpr int kMmaWarp = 4, kLoadK = 5, kLoadV = 6;
-constexpr int kThreads = 7 * 32;
+constexpr int kMmaWarp = 4, kLoadK = 5, kLoadV = 6, kItemWarp = 7;
+constexpr int kThreads = 8 * 32;
 constexpr int kQMax = 8355711;                 // 127 * 65536 + 127 * 256 + 127, three signed digits
 constexpr float kQUnit = 8355711.f;
 constexpr float kWUnit = 16777215.f;           // 2^24 - 1
 
-// V: virtual heads of the CTA (query heads, twice that at head_dim 64).
+// An item, as warp 7 hands it to the others.
+struct Item {
+    int ntiles;   // -1: no more items
+    int s;
+    int head0;    // its first query head
+    int kvh;
+    int first;    // its tokens: first .. end - 1
+    int end;
+    int part;
+    int write;    // whether it has an output (else it is skipped)
+    int ids[kMaxBlocks];  // blocks of the first tile (-1: none)
+};
+
+struct Scales {
+    float k[kMaxBlocks], v[kMaxBlocks];
+    unsigned valid;  // bit i: block i of the tile is one
+    unsigned pad[3];
+};
+
+// V: virtual heads of an item (query heads, twice that at head_dim 64). The
+// digit rows a product reads past 3 V (up to kN) only give columns that nobody
+// reads, so those rows are whatever lies behind.
 template <int V> struct Shape {
-    static constexpr int kN = (3 * V + 15) / 16 * 16;  // MMA columns
+    static constexpr int kN = (3 * V + 15) / 16 * 16;          // MMA columns
+    static constexpr int kDigits = (3 * V + 7) / 8 * 1024;     // bytes of 3 V digit rows, in 8-row groups
     static constexpr int kOffK = 0;
     static constexpr int kOffV = kOffK + kStages * kTile;
-    static constexpr int kOffQ = kOffV + kStages * kTile;     // [kN][128] signed digits
-    static constexpr int kOffP = kOffQ + kN * kRowBytes;      // [kN][128] unsigned digits
-    static constexpr int kOffMax = kOffP + kN * kRowBytes;    // float [2][4 warps][V], tiles in turn
-    static constexpr int kOffQs = kOffMax + 8 * V * 4;        // float [V]: log2 score per unit of digits and k_scale
-    static constexpr int kOffBar = (kOffQs + V * 4 + 7) / 8 * 8;
-    static constexpr int kBars = 4 * kStages + 2 + 4;         // k/v full/empty, s_full[2], p_full, o_full, q_full, idle
-    static constexpr int kSmemBytes = 1024 + kOffBar + kBars * 8 + 16;
+    static constexpr int kOffQ = kOffV + kStages * kTile;      // [kItems] signed digits
+    static constexpr int kOffP = kOffQ + kItems * kDigits;     // unsigned digits; between items the threads' sums
+    static constexpr int kOffScales = kOffP + kDigits;
+    static constexpr int kOffItems = kOffScales + kScales * (int)sizeof(Scales);
+    static constexpr int kOffQs = kOffItems + kItems * (int)sizeof(Item);  // float [kItems][V]: log2 score per digit unit
+    static constexpr int kOffMax = kOffQs + kItems * V * 4;    // float [2][4 warps][V], tiles in turn
+    static constexpr int kOffClc = (kOffMax + 8 * V * 4 + 15) / 16 * 16;
+    static constexpr int kOffBar = kOffClc + 16;
+    static constexpr int kBars = 4 * kStages + 2 + 4 + 2 * kItems + 1;
+    static constexpr int kEnd = kOffBar + kBars * 8 + 16;
+    static constexpr int kReadEnd = kOffP + kN * kRowBytes;    // the last byte a product may read
+    static constexpr int kSmemBytes = kEnd > kReadEnd ? kEnd : kReadEnd;
     // tensor memory: S in two buffers, O in one
     static constexpr int kSCol = 0, kOCol = 2 * kN;
     static constexpr int kCols = 3 * kN <= 64 ? 64 : 3 * kN <= 128 ? 128 : 256;
-    // three CTAs an SM for up to 8 virtual heads, two for 16 (by shared memory as well as tensor memory)
+    // CTAs per SM: three, by shared memory; two for 16 virtual heads (tensor memory), held to it by registers
     static constexpr int kCtas = kCols <= 128 ? 3 : 2;
-    static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024 && (kCtas + 1) * (kSmemBytes + 1024) > 228 * 1024, "CTAs per SM");
-    static_assert(kCtas * kCols <= 512, "tensor memory");
+    // registers: of the launch, and after warps 4-7 have given theirs to warps 0-3
+    static constexpr int kRegs = kCtas == 3 ? 80 : 128;
+    static constexpr int kRegsLow = 40, kRegsHigh = kCtas == 3 ? 120 : 216;
+    static_assert(kRegsLow + kRegsHigh <= 2 * kRegs, "registers taken over are registers given up");
+    static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "CTAs per SM");
+    static_assert(kCtas * kCols <= 512 && (kCtas + 1) * kRegs * kThreads > 65536, "tensor memory for every resident CTA");
+    static_assert(8 * V * 4 + (V > 1 ? V / 2 : 1) * 64 * 4 <= kDigits, "the threads' sums fit the weights' digits");
 };
 
 // ------------------------------------------------------------- tensor cores
@@ -130,6 +176,19 @@ __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a, uint64_t b, 
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
                  : "memory");
+}
+
+// Whether the barrier's phase is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -174,6 +233,40 @@ __device__ __forceinline__ float warp_max(float x) {
     return y;
 }
 
+// Registers per thread of this warpgroup, given up or taken over.
+template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Asks for a block of the grid that has not started; the 16-byte answer completes on bar.
+__device__ __forceinline__ void try_cancel(void *answer, uint64_t *bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            smem_addr(answer)),
+        "r"(smem_addr(bar))
+        : "memory");
+}
+
+// Whether the answer is a block, and which.
+__device__ __forceinline__ bool canceled(const void *answer, int &x, int &y, int &z) {
+    uint32_t ok, cx, cy, cz;
+    asm volatile(
+        "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 a, [%4];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::y.b32.b128 %2, a;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::z.b32.b128 %3, a;\n\t}"
+        : "=r"(ok), "=r"(cx), "=r"(cy), "=r"(cz)
+        : "r"(smem_addr(answer))
+        : "memory");
+    x = (int)cx;
+    y = (int)cy;
+    z = (int)cz;
+    return ok != 0;
+}
+
 // ------------------------------------------------------------------- kernel
 
 template <typename T, int D, int G>
@@ -188,63 +281,56 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
     constexpr int kOCols3 = (3 * G + 3) / 4 * 4;  // O columns read: those of the lane's own tokens
     constexpr int kTok = 128 * kPar;              // tokens per tile
 
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char *sm =
-        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    unsigned char *Qs = sm + Sh::kOffQ, *Ps = sm + Sh::kOffP;
-    float *wmax = reinterpret_cast<float *>(sm + Sh::kOffMax);
+    extern __shared__ __align__(1024) unsigned char sm[];
+    unsigned char *Ps = sm + Sh::kOffP;
+    Scales *scales = reinterpret_cast<Scales *>(sm + Sh::kOffScales);
+    Item *items = reinterpret_cast<Item *>(sm + Sh::kOffItems);
     float *qscale = reinterpret_cast<float *>(sm + Sh::kOffQs);
+    float *wmax = reinterpret_cast<float *>(sm + Sh::kOffMax);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Sh::kOffBar);
-    uint64_t *k_full = bars, *v_full = bars + kStages;              // a stage's tile has landed
+    uint64_t *k_full = bars, *v_full = bars + kStages;              // a stage's tile (and its scales) is there
     uint64_t *k_empty = bars + 2 * kStages, *v_empty = bars + 3 * kStages;  // the product that read it is done
-    uint64_t *s_full = bars + 4 * kStages;                          // [2] S_j computed
-    uint64_t *p_full = s_full + 2;                                  // P_j written (and S_j, O_{j-1} read)
-    uint64_t *o_full = s_full + 3;                                  // O_j computed
-    uint64_t *q_full = s_full + 4;                                  // the query's digits are written
-    uint64_t *idle = s_full + 5;                                    // every product issued has finished
+    uint64_t *s_full = bars + 4 * kStages;   // [2] S of the tile computed
+    uint64_t *p_full = s_full + 2;           // weights of the tile written (its S and the O before it read)
+    uint64_t *o_full = s_full + 3;           // O of the tile computed
+    uint64_t *idle = s_full + 4;             // every product issued has finished
+    uint64_t *clc = s_full + 5;              // the answer to a claim
+    uint64_t *claim = s_full + 6;            // warp 5 nears the end of an item: claim the next
+    uint64_t *i_full = s_full + 7, *i_empty = i_full + kItems;  // an item is described; everybody is done with it
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Sh::kBars);
     volatile int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int s = blockIdx.z;
-    if (p.seq_order) {
-        s = __ldg(p.seq_order + s);
-        if (s < 0 || s >= p.num_seqs) {
-            if (tid == 0) record_error(p.err, PA_DEVERR_CONTEXT);
-            return;
-        }
-    }
-    const int kvh = blockIdx.y / p.sub_groups, sub = blockIdx.y % p.sub_groups;
-    const int head0 = kvh * p.group + sub * kG, g_valid = min(G, p.group - sub * kG);
-    int L = __ldg(p.ctx + s);
-    const int room = (int)min((long long)p.max_blocks << p.bs_shift, (long long)p.max_ctx);
-    if (L < 0 || L > room) {
-        if (tid == 0) record_error(p.err, PA_DEVERR_CONTEXT);
-        L = L < 0 ? 0 : room;
-    }
-    // this CTA's tokens: first .. L - 1, tiles of kTok
-    const int first = blockIdx.x * p.partition_size;
-    if (p.partition_size) {
-        L = min(L, first + p.partition_size);
-        if (first >= L) return;  // no such partition: its entry is not read
-    }
-    const size_t row0 = (size_t)s * p.num_heads + head0;  // output row of head 0
-    if (L <= 0) {
-        for (int i = tid; i < g_valid * D; i += kThreads) store_out(p.out, row0 * D + i, 0.f, p.out_dtype);
+    const int bs_shift = p.bs_shift;
+    const int blocks = kTok >> bs_shift;      // per tile: 4, 8 or 16
+    const int rows = 128 / blocks;            // 128-byte rows of a block
+    auto give_up = [&]() {
+        record_error(p.err, PA_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+    };
+
+    if (smem_addr(sm) & 1023u) {  // the swizzled layouts count on it
+        if (tid == 0) record_error(p.err, PA_DEVERR_TIMEOUT);
         return;
     }
-    const int ntiles = (L - first + kTok - 1) / kTok;
-    const int32_t *trow = p.tables + (size_t)s * p.max_blocks;
-    const int bs_shift = p.bs_shift;
-
     if (tid == 0) {
-        for (int i = 0; i < 4 * kStages; ++i) mbar_init(bars + i, 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(k_full + i, 2);
+            mbar_init(v_full + i, 1);
+            mbar_init(k_empty + i, 1);
+            mbar_init(v_empty + i, 1);
+        }
         mbar_init(s_full, 1);
         mbar_init(s_full + 1, 1);
         mbar_init(p_full, kSoftmaxThreads);
         mbar_init(o_full, 1);
-        mbar_init(q_full, kSoftmaxThreads);
         mbar_init(idle, 1);
+        mbar_init(clc, 1);
+        mbar_init(claim, 1);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(i_full + i, 1);
+            mbar_init(i_empty + i, 7);  // warps 0-6
+        }
         *abort_flag = 0;
         fence_mbar_init();
         fence_proxy_async_smem();
@@ -255,279 +341,410 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // digit columns past the heads, and padding heads, stay zero
-    for (int i = tid; i < 2 * kN * kRowBytes / 16; i += kThreads)
-        reinterpret_cast<uint4 *>(Qs)[i] = make_uint4(0u, 0u, 0u, 0u);
-    fence_proxy_async_smem();  // each thread's zeros, before the products read them
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp >= kLoadK) {
-        // ====================================================== load warps
-        // Lane i brings block i of the tile: kBoxRows rows of 128 bytes.
-        const bool is_v = warp == kLoadV;
-        const CUtensorMap *map = is_v ? &v_map : &k_map;
-        uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
-        unsigned char *ring = sm + (is_v ? Sh::kOffV : Sh::kOffK);
-        const int blocks = kTok >> bs_shift;         // per tile: 4, 8 or 16
-        const int rows = 128 / blocks;               // 128-byte rows of a block
-        const int b0 = first >> bs_shift, nblk = (L + (1 << bs_shift) - 1) >> bs_shift;
-        auto look = [&](int j) -> int {
-            const int lb = b0 + j * blocks + lane;
-            return (lane < blocks && lb < nblk) ? __ldg(trow + lb) : -1;
-        };
-        int id = look(0), id_next = look(1);
-        int issued = 0;
-        for (int j = 0; j < ntiles; ++j) {
-            const int b = j % kStages;
-            if (j >= kStages) {
-                const bool got = mbar_wait(empty + b, (j / kStages - 1) & 1) && !*abort_flag;
-                if (!__all_sync(0xffffffffu, got)) {
+    if (warp >= 4) {
+        regs_dec<Sh::kRegsLow>();
+        if (warp == kItemWarp) {
+            // ======================================================= item warp
+            int x = blockIdx.x, y = blockIdx.y, z = blockIdx.z;
+            bool more = true, sound = true;
+            for (int n = 0; sound; ++n) {
+                const int slot = n % kItems;
+                if (n >= kItems) {
+                    sound = __all_sync(0xffffffffu, mbar_wait(i_empty + slot, (n / kItems - 1) & 1) && !*abort_flag);
+                    if (!sound) break;
+                }
+                Item &it = items[slot];
+                if (!more) {
                     if (lane == 0) {
-                        record_error(p.err, PA_DEVERR_TIMEOUT);
-                        *abort_flag = 1;
+                        it.ntiles = -1;
+                        mbar_arrive(i_full + slot);
                     }
                     break;
                 }
-            }
-            const bool here = lane < blocks && b0 + j * blocks + lane < nblk;
-            const bool ok = here && id >= 0 && id < p.num_blocks;
-            if (here && !ok) record_error(p.err, PA_DEVERR_BLOCK_ID);
-            const unsigned m = __ballot_sync(0xffffffffu, ok);
-            if (lane == 0) mbar_arrive_expect_tx(full + b, __popc(m) * rows * kRowBytes);
-            __syncwarp();
-            if (ok)
-                tma_load_2d(ring + b * kTile + lane * rows * kRowBytes, map, 0, (id * p.num_kv_heads + kvh) * rows,
-                            full + b);
-            ++issued;
-            id = id_next;
-            id_next = look(j + 2);
-        }
-        // copies in flight land before the CTA leaves
-        for (int j = max(0, issued - kStages); j < issued; ++j) mbar_wait(full + j % kStages, (j / kStages) & 1);
-        __syncwarp();
-    } else if (warp == kMmaWarp) {
-        // ======================================================== MMA warp
-        if (lane == 0) {
-            constexpr uint32_t kIdQK = idesc_i8(true, false, kN), kIdPV = idesc_i8(false, true, kN);
-            const uint32_t qa = smem_addr(Qs), pa_ = smem_addr(Ps);
-            bool ok = mbar_wait(q_full, 0) && !*abort_flag;
-            auto issue_s = [&](int j) -> bool {
-                const int b = j % kStages;
-                if (!mbar_wait(k_full + b, (j / kStages) & 1) || *abort_flag) return false;
-                fence_after();
-                const uint32_t ka = smem_addr(sm + Sh::kOffK) + b * kTile;
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_i8(tmem + Sh::kSCol + (j & 1) * kN, desc128(ka + kk * 32), desc128(qa + kk * 32), kIdQK, kk > 0);
-                mma_commit(s_full + (j & 1));
-                mma_commit(k_empty + b);
-                return true;
-            };
-            for (int j = 0; ok && j < min(2, ntiles); ++j) ok = issue_s(j);
-            for (int j = 0; ok && j < ntiles; ++j) {
-                const int b = j % kStages;
-                if (!mbar_wait(p_full, j & 1) || !mbar_wait(v_full + b, (j / kStages) & 1) || *abort_flag) {
-                    ok = false;
-                    break;
+                // ---- the item
+                int s = z, write = 1;
+                if (p.seq_order) {
+                    s = __ldg(p.seq_order + z);
+                    if (s < 0 || s >= p.num_seqs) {
+                        if (lane == 0) record_error(p.err, PA_DEVERR_CONTEXT);
+                        s = 0;
+                        write = 0;
+                    }
                 }
-                fence_after();
-                const uint32_t va = smem_addr(sm + Sh::kOffV) + b * kTile;
+                const int kvh = y / p.sub_groups, sub = y % p.sub_groups;
+                const int head0 = kvh * p.group + sub * kG, g_valid = min(G, p.group - sub * kG);
+                // the query's raw values, while the lengths come
+                constexpr int kE = D / 32;
+                using Raw = std::conditional_t<kE == 4, uint2, uint32_t>;  // a lane's kE values
+                Raw raw[G];
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_i8(tmem + Sh::kOCol, desc128(va + kk * 32 * kRowBytes), desc128(pa_ + kk * 32), kIdPV, kk > 0);
-                mma_commit(o_full);
-                mma_commit(v_empty + b);
-                if (j + 2 < ntiles) ok = issue_s(j + 2);
+                for (int g = 0; g < G; ++g) {
+                    raw[g] = Raw{};
+                    if (g < g_valid)
+                        raw[g] = __ldg(reinterpret_cast<const Raw *>(static_cast<const T *>(p.query) +
+                                                                     ((size_t)s * p.num_heads + head0 + g) * D) + lane);
+                }
+                int L = __ldg(p.ctx + s);
+                const int room = (int)min((long long)p.max_blocks << bs_shift, (long long)p.max_ctx);
+                if (write && (L < 0 || L > room)) {
+                    if (lane == 0) record_error(p.err, PA_DEVERR_CONTEXT);
+                    L = L < 0 ? 0 : room;
+                }
+                const int first = x * p.partition_size;
+                if (p.partition_size) {
+                    L = min(L, first + p.partition_size);
+                    if (first >= L) write = 0;  // no such partition: its entry is not read
+                }
+                if (!write) L = first;
+                const int ntiles = L > first ? (L - first + kTok - 1) / kTok : 0;
+                const int lb = (first >> bs_shift) + lane, nblk = (L + (1 << bs_shift) - 1) >> bs_shift;
+                const int id = ntiles && lane < blocks && lb < nblk ? __ldg(p.tables + (size_t)s * p.max_blocks + lb) : -1;
+                if (lane < kMaxBlocks) it.ids[lane] = id;
+                if (lane == 0) {
+                    it.ntiles = ntiles;
+                    it.s = s;
+                    it.head0 = head0;
+                    it.kvh = kvh;
+                    it.first = first;
+                    it.end = L;
+                    it.part = x;
+                    it.write = write;
+                }
+                // ---- the query's digits
+                unsigned char *Qs = sm + Sh::kOffQ + slot * Sh::kDigits;
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const T *raw_g = reinterpret_cast<const T *>(&raw[g]);
+                    float q[kE], amax = 0.f, odd = 0.f;  // odd: NaN if an element is not finite
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) {
+                        q[e] = (float)raw_g[e];
+                        amax = fmaxf(amax, fabsf(q[e]));
+                        odd += q[e] * 0.f;
+                    }
+                    amax = warp_max(amax);
+#pragma unroll
+                    for (int mk = 16; mk >= 1; mk >>= 1) odd += __shfl_xor_sync(0xffffffffu, odd, mk);
+                    // a query below 2^-100 counts as zero (its unit's reciprocal would not be finite)
+                    const bool live = amax >= 7.888609e-31f && odd == 0.f;
+                    const float inv = live ? kQUnit / amax : 0.f;
+                    uint32_t w[3] = {0u, 0u, 0u};  // the lane's kE digits of each place
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) {
+                        // (the product may round up past the unit)
+                        const int v = live ? max(-kQMax, min(kQMax, __float2int_rn(q[e] * inv))) : 0;
+                        const int c = (int)(int8_t)v, v1 = (v - c) >> 8;
+                        const int b = (int)(int8_t)v1, a = (v1 - b) >> 8;
+                        w[0] |= (uint32_t)(a & 0xff) << (8 * e);
+                        w[1] |= (uint32_t)(b & 0xff) << (8 * e);
+                        w[2] |= (uint32_t)(c & 0xff) << (8 * e);
+                    }
+#pragma unroll
+                    for (int par = 0; par < kPar; ++par)
+#pragma unroll
+                        for (int i = 0; i < 3; ++i) {
+                            const int r = (par * G + g) * 3 + i;  // digit row; its 16-byte chunks are swizzled
+                            auto at = [&](int half) {
+                                return Qs + r * kRowBytes + ((half * D + lane * kE) ^ ((r & 7) << 4));
+                            };
+                            if constexpr (kPar == 1) {
+                                *reinterpret_cast<uint32_t *>(at(0)) = w[i];
+                            } else {
+                                *reinterpret_cast<uint16_t *>(at(par)) = (uint16_t)w[i];
+                                *reinterpret_cast<uint16_t *>(at(1 - par)) = 0;
+                            }
+                        }
+                    if (lane < kPar) qscale[slot * kV + lane * G + g] = (live ? amax / kQUnit : 0.f) * p.scale_log2 + odd;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(i_full + slot);
+                // ---- the next one, once warp 5 is near the end of this one
+                more = false;
+                if (p.steal) {
+                    sound = __all_sync(0xffffffffu, mbar_wait(claim, n & 1) && !*abort_flag);
+                    if (!sound) break;
+                    if (lane == 0) {
+                        fence_proxy_async_smem();  // the last answer has been read
+                        mbar_arrive_expect_tx(clc, 16);
+                        try_cancel(sm + Sh::kOffClc, clc);
+                    }
+                    sound = __all_sync(0xffffffffu, mbar_wait(clc, n & 1));
+                    if (sound) more = canceled(sm + Sh::kOffClc, x, y, z);
+                    __syncwarp();
+                }
             }
-            if (!ok) {
-                record_error(p.err, PA_DEVERR_TIMEOUT);
-                *abort_flag = 1;
+            if (!sound && lane == 0) give_up();
+        } else if (warp != kMmaWarp) {
+            // ======================================================= load warps
+            // Lane i brings block i of the tile: `rows` rows of 128 bytes.
+            static_assert(kLoadK + 1 == kLoadV, "two load warps");
+            const bool is_v = warp == kLoadV;
+            const CUtensorMap *map = is_v ? &v_map : &k_map;
+            uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
+            unsigned char *ring = sm + (is_v ? Sh::kOffV : Sh::kOffK);
+            int t = 0;  // tiles loaded, over all items
+            bool sound = true;
+            for (int n = 0; sound; ++n) {
+                const int slot = n % kItems;
+                sound = __all_sync(0xffffffffu, mbar_wait(i_full + slot, (n / kItems) & 1) && !*abort_flag);
+                if (!sound) break;
+                const Item &it = items[slot];
+                const int ntiles = it.ntiles;
+                if (ntiles < 0) break;
+                const int kvh = it.kvh, b0 = it.first >> bs_shift;
+                const int nblk = (it.end + (1 << bs_shift) - 1) >> bs_shift;
+                const int32_t *trow = p.tables + (size_t)it.s * p.max_blocks;
+                int id = lane < kMaxBlocks ? it.ids[lane] : -1;
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(i_empty + slot);
+                    if (!is_v && p.steal && ntiles < 4) mbar_arrive(claim);
+                }
+                auto look = [&](int j) -> int {
+                    const int lb = b0 + j * blocks + lane;
+                    return (lane < blocks && lb < nblk) ? __ldg(trow + lb) : -1;
+                };
+                auto scale_of = [&](const float *scale, int block) -> float {
+                    return !is_v && block >= 0 && block < p.num_blocks
+                               ? __ldg(scale + (size_t)block * p.num_kv_heads + kvh) : 0.f;
+                };
+                int id_next = ntiles > 1 ? look(1) : -1;
+                float ks = scale_of(p.k_scale, id), vs = scale_of(p.v_scale, id);
+                for (int j = 0; j < ntiles; ++j, ++t) {
+                    const int b = t % kStages;
+                    if (t >= kStages) {
+                        sound = __all_sync(0xffffffffu, mbar_wait(empty + b, (t / kStages - 1) & 1) && !*abort_flag);
+                        if (!sound) break;
+                    }
+                    const bool here = lane < blocks && b0 + j * blocks + lane < nblk;
+                    const bool ok = here && id >= 0 && id < p.num_blocks;
+                    if (here && !ok && !is_v) record_error(p.err, PA_DEVERR_BLOCK_ID);
+                    const unsigned m = __ballot_sync(0xffffffffu, ok);
+                    if (lane == 0) mbar_arrive_expect_tx(full + b, __popc(m) * rows * kRowBytes);
+                    __syncwarp();
+                    if (ok)
+                        tma_load_2d(ring + b * kTile + lane * rows * kRowBytes, map, 0, (id * p.num_kv_heads + kvh) * rows,
+                                    full + b);
+                    if (!is_v) {
+                        Scales &sc = scales[t % kScales];
+                        if (lane < kMaxBlocks) {
+                            sc.k[lane] = ks;
+                            sc.v[lane] = vs;
+                        }
+                        if (lane == 0) sc.valid = m;
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(full + b);
+                            if (p.steal && ntiles >= 4 && j == ntiles - 4) mbar_arrive(claim);
+                        }
+                    }
+                    id = id_next;
+                    ks = scale_of(p.k_scale, id);
+                    vs = scale_of(p.v_scale, id);
+                    id_next = look(j + 2);
+                }
             }
-            // tensor memory is freed below: every product issued must have finished
-            mma_commit(idle);
-            if (!mbar_wait(idle, 0)) record_error(p.err, PA_DEVERR_TIMEOUT);
+            if (!sound && lane == 0) give_up();
+            // copies in flight land before the CTA leaves
+            for (int i = max(0, t - kStages); i < t; ++i) mbar_wait(full + i % kStages, (i / kStages) & 1);
+            __syncwarp();
+        } else {
+            // ========================================================= MMA warp
+            if (lane == 0) {
+                constexpr uint32_t kIdQK = idesc_i8(true, false, kN), kIdPV = idesc_i8(false, true, kN);
+                const uint32_t base = smem_addr(sm);
+                int n = -1, left = 0, slot = 0;  // the item whose S is issued next, and its tiles to come
+                int issued = 0, done = 0;        // tiles whose S, whose O has been issued
+                bool sound = true, more = true;
+                while (sound) {
+                    if (more && left == 0 && issued < done + 2) {
+                        // The next item. It may be described only after an item has
+                        // ended whose O is still to be issued here, so that goes first.
+                        const int next = (n + 1) % kItems;
+                        if (done == issued || mbar_test(i_full + next, ((n + 1) / kItems) & 1)) {
+                            sound = mbar_wait(i_full + next, ((n + 1) / kItems) & 1) && !*abort_flag;
+                            if (!sound) break;
+                            if (n >= 0) mbar_arrive(i_empty + slot);
+                            ++n;
+                            slot = next;
+                            left = items[slot].ntiles;
+                            if (left < 0) {
+                                more = false;
+                                left = 0;
+                            }
+                            continue;
+                        }
+                    }
+                    if (left > 0 && issued < done + 2) {
+                        const int b = issued % kStages;
+                        sound = mbar_wait(k_full + b, (issued / kStages) & 1) && !*abort_flag;
+                        if (!sound) break;
+                        fence_after();
+                        const uint32_t ka = base + Sh::kOffK + b * kTile, qa = base + Sh::kOffQ + slot * Sh::kDigits;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_i8(tmem + Sh::kSCol + (issued & 1) * kN, desc128(ka + kk * 32), desc128(qa + kk * 32), kIdQK,
+                                   kk > 0);
+                        mma_commit(s_full + (issued & 1));
+                        mma_commit(k_empty + b);
+                        ++issued;
+                        --left;
+                        continue;
+                    }
+                    if (done == issued) break;  // no more items (with some, the next one was taken above)
+                    const int b = done % kStages;
+                    sound = mbar_wait(p_full, done & 1) && mbar_wait(v_full + b, (done / kStages) & 1) && !*abort_flag;
+                    if (!sound) break;
+                    fence_after();
+                    const uint32_t va = base + Sh::kOffV + b * kTile, pa_ = base + Sh::kOffP;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_i8(tmem + Sh::kOCol, desc128(va + kk * 32 * kRowBytes), desc128(pa_ + kk * 32), kIdPV, kk > 0);
+                    mma_commit(o_full);
+                    mma_commit(v_empty + b);
+                    ++done;
+                }
+                if (!sound) give_up();
+                // tensor memory is freed below: every product issued must have finished
+                mma_commit(idle);
+                if (!mbar_wait(idle, 0)) record_error(p.err, PA_DEVERR_TIMEOUT);
+            }
+            __syncwarp();
         }
-        __syncwarp();
     } else {
         // =================================================== softmax warps
+        regs_inc<Sh::kRegsHigh>();
         const int r = tid;
         const uint32_t tlane = tmem + ((uint32_t)(warp * 32) << 16);
-        // ---- the query's digits: warp w takes heads w, w + 4
-#pragma unroll
-        for (int g0 = 0; g0 < G; g0 += 4) {
-            const int g = g0 + warp;
-            if (g < G) {
-                constexpr int kE = D / 32;
-                float x[kE];
-                float amax = 0.f, odd = 0.f;  // odd: NaN if an element is not finite
-#pragma unroll
-                for (int e = 0; e < kE; ++e) {
-                    x[e] = g < g_valid ? (float)static_cast<const T *>(p.query)[(row0 + g) * D + lane * kE + e] : 0.f;
-                    amax = fmaxf(amax, fabsf(x[e]));
-                    odd += x[e] * 0.f;
-                }
-                amax = warp_max(amax);
-#pragma unroll
-                for (int mk = 16; mk >= 1; mk >>= 1) odd += __shfl_xor_sync(0xffffffffu, odd, mk);
-                // a query below 2^-100 counts as zero (its unit's reciprocal would not be finite)
-                const bool live = amax >= 7.888609e-31f && odd == 0.f;
-                const float inv = live ? kQUnit / amax : 0.f;
-#pragma unroll
-                for (int e = 0; e < kE; ++e) {
-                    // (the product may round up past the unit)
-                    const int q = live ? max(-kQMax, min(kQMax, __float2int_rn(x[e] * inv))) : 0;
-                    const int c = (int)(int8_t)q, q1 = (q - c) >> 8;
-                    const int b = (int)(int8_t)q1, a = (q1 - b) >> 8;
-#pragma unroll
-                    for (int par = 0; par < kPar; ++par) {
-                        const int n = (par * G + g) * 3, at = par * D + lane * kE + e;
-                        Qs[n * kRowBytes + (at ^ ((n & 7) << 4))] = (unsigned char)a;
-                        Qs[(n + 1) * kRowBytes + (at ^ (((n + 1) & 7) << 4))] = (unsigned char)b;
-                        Qs[(n + 2) * kRowBytes + (at ^ (((n + 2) & 7) << 4))] = (unsigned char)c;
-                    }
-                }
-                if (lane < kPar) qscale[lane * G + g] = (live ? amax / kQUnit : 0.f) * p.scale_log2 + odd;
-            }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(q_full);
-        named_bar_sync(1, kSoftmaxThreads);
-        float qs[kV];
-#pragma unroll
-        for (int v = 0; v < kV; ++v) qs[v] = qscale[v];
-
-        // ---- tiles. The scales of row r's block come two tiles ahead (its id) and one tile ahead.
-        const int nblk = (L + (1 << bs_shift) - 1) >> bs_shift;
-        auto look = [&](int j) -> int {
-            const int lb = (first + j * kTok + r * kPar) >> bs_shift;
-            const int id = (j < ntiles && lb < nblk) ? __ldg(trow + lb) : -1;
-            return id < p.num_blocks ? id : -1;
-        };
-        float ks = 0.f, vs = 0.f;
-        int id = look(0), id_next = look(1);
-        if (id >= 0) {
-            ks = __ldg(p.k_scale + (size_t)id * p.num_kv_heads + kvh);
-            vs = __ldg(p.v_scale + (size_t)id * p.num_kv_heads + kvh);
-        }
-        float m_l[kV], l[kV];            // this thread's tokens: largest score, sum of 2^(score - it)
-        float m_o[G], o[G], m_tile[G];   // O of the lane's dim: sum * 2^-m_o; the unit of the tile in tensor memory
-#pragma unroll
-        for (int v = 0; v < kV; ++v) {
-            m_l[v] = -INFINITY;
-            l[v] = 0.f;
-        }
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            m_o[g] = m_tile[g] = -INFINITY;
-            o[g] = 0.f;
-        }
-        const int par0 = kPar == 2 ? (warp >> 1) * G : 0;  // first virtual head of this lane's tokens
-        // adds the tile in tensor memory (its O columns, in units of 2^m_tile / kWUnit) to o
-        auto add_tile = [&]() {
-            int t[kOCols3];
-            tmem_load<kOCols3>(tlane + Sh::kOCol + 3 * par0, t);
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const float f = fmaf((float)t[3 * g], 65536.f, (float)(t[3 * g + 1] * 256 + t[3 * g + 2]));
-                if (m_tile[g] > m_o[g]) {  // the same in every thread of the warp
-                    o[g] = o[g] * fast_exp2(m_o[g] - m_tile[g]) + f;
-                    m_o[g] = m_tile[g];
-                } else if (m_tile[g] > -INFINITY) {
-                    o[g] = fmaf(f, fast_exp2(m_tile[g] - m_o[g]), o[g]);
-                }
-            }
-        };
-        // The four warps leave the loop together: one whose wait ran out says so
-        // at the tile's barrier.
-        bool sound = true, ok = true;
-        for (int j = 0; j < ntiles; ++j) {
-            // the next tile's scales
-            float ks_next = 0.f, vs_next = 0.f;
-            if (id_next >= 0) {
-                ks_next = __ldg(p.k_scale + (size_t)id_next * p.num_kv_heads + kvh);
-                vs_next = __ldg(p.v_scale + (size_t)id_next * p.num_kv_heads + kvh);
-            }
-            const int id_after = look(j + 2);
-            const float lv = vs > 0.f ? log2f(vs) : -INFINITY;
-            const int tok = first + j * kTok + r * kPar;
-            float *wm = wmax + (j & 1) * 4 * kV;
-
-            sound = __all_sync(0xffffffffu, sound && mbar_wait(s_full + (j & 1), (j >> 1) & 1) && !*abort_flag);
-            float x[kV];  // log2 of the weight
-            if (sound) {
-                fence_after();
-                int t[kCols3];
-                tmem_load<kCols3>(tlane + Sh::kSCol + (j & 1) * kN, t);
-#pragma unroll
-                for (int v = 0; v < kV; ++v) {
-                    const float f = fmaf((float)t[3 * v], 65536.f, (float)(t[3 * v + 1] * 256 + t[3 * v + 2]));
-                    const float sc = f * (qs[v] * ks);
-                    const bool live = id >= 0 && tok + v / G < L;
-                    if (live) {
-                        const float d = sc - m_l[v];
-                        const float e = fast_exp2(-fabsf(d));
-                        l[v] = d > 0.f ? fmaf(l[v], e, 1.f) : l[v] + e;
-                        m_l[v] = fmaxf(m_l[v], sc);
-                    }
-                    x[v] = live ? sc + lv : -INFINITY;
-                }
-                // the tile's largest weight per head, over this warp
-#pragma unroll
-                for (int v = 0; v < kV; ++v) {
-                    const float mw = warp_max(x[v]);
-                    if (lane == 0) wm[warp * kV + v] = mw;
-                }
-            }
+        const int block = r / rows;                        // this row's block within a tile
+        const int par0 = kPar == 2 ? (warp >> 1) * G : 0;  // first virtual head of this lane's head dim
+        float *red_m = reinterpret_cast<float *>(Ps), *red_l = red_m + 4 * kV;
+        float *red_o = red_l + 4 * kV;  // [G][64]: the odd tokens' sums at head_dim 64
+        int t = 0;                      // tiles done, over all items
+        // The four warps leave the loops together: one whose wait ran out says
+        // so at the next barrier of all four.
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            const int slot = n % kItems;
+            bool sound = __all_sync(0xffffffffu, mbar_wait(i_full + slot, (n / kItems) & 1) && !*abort_flag);
             ok = softmax_sync_and(sound);
             if (!ok) break;
-            float mt[kV];
+            const Item &it = items[slot];
+            const int ntiles = it.ntiles;
+            if (ntiles < 0) break;
+            const int L = it.end, first = it.first, part = it.part, write = it.write;
+            const size_t row0 = (size_t)it.s * p.num_heads + it.head0;  // output row of head 0
+            const int g_valid = min(G, p.group - it.head0 % p.group / kG * kG);
+            float qs[kV];
 #pragma unroll
-            for (int v = 0; v < kV; ++v)
-                mt[v] = fmaxf(fmaxf(wm[v], wm[kV + v]), fmaxf(wm[2 * kV + v], wm[3 * kV + v]));
-            if (j > 0) {  // O_{j-1} is there: P and O are free once it is added up
-                sound = __all_sync(0xffffffffu, mbar_wait(o_full, (j - 1) & 1) && !*abort_flag);
-                if (!sound) continue;  // (the next tile's barrier, or the one behind the loop, tells the others)
-                fence_after();
-                add_tile();
-            }
-#pragma unroll
-            for (int g = 0; g < G; ++g) m_tile[g] = kPar == 2 && par0 ? mt[kV - G + g] : mt[g];
-            // ---- the weights' digits, column 3 v + i, byte r of the row (its 16-byte chunk swizzled)
+            for (int v = 0; v < kV; ++v) qs[v] = qscale[slot * kV + v];
+            float m_l[kV], l[kV];            // this thread's tokens: largest score, sum of 2^(score - it)
+            float m_o[G], o[G], m_tile[G];   // O of the lane's dim: sum * 2^-m_o; the unit of the tile in tensor memory
 #pragma unroll
             for (int v = 0; v < kV; ++v) {
-                const float w = x[v] > -INFINITY ? fast_exp2(x[v] - mt[v]) : 0.f;
-                const unsigned u = __float2uint_rn(w * kWUnit);
-                const int n = 3 * v;
-                Ps[n * kRowBytes + (r ^ ((n & 7) << 4))] = (unsigned char)(u >> 16);
-                Ps[(n + 1) * kRowBytes + (r ^ (((n + 1) & 7) << 4))] = (unsigned char)(u >> 8);
-                Ps[(n + 2) * kRowBytes + (r ^ (((n + 2) & 7) << 4))] = (unsigned char)u;
+                m_l[v] = -INFINITY;
+                l[v] = 0.f;
             }
-            fence_proxy_async_smem();
-            fence_before();
-            mbar_arrive(p_full);
-            id = id_next;
-            id_next = id_after;
-            ks = ks_next;
-            vs = vs_next;
-        }
-        if (ok) {
-            sound = __all_sync(0xffffffffu, sound && mbar_wait(o_full, (ntiles - 1) & 1) && !*abort_flag);
-            if (sound) {
-                fence_after();
-                add_tile();
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                m_o[g] = m_tile[g] = -INFINITY;
+                o[g] = 0.f;
             }
-            ok = softmax_sync_and(sound);
-        }
-        // ---- the threads' sums, and the output. Every product is done (o_full),
-        // so the K tiles are free to hold them.
-        float *red_m = reinterpret_cast<float *>(sm), *red_l = red_m + 4 * kV;
-        float *red_o = red_l + 4 * kV;  // [G][64]: the odd tokens' sums at head_dim 64
-        if (!ok) {
-            if (r == 0) record_error(p.err, PA_DEVERR_TIMEOUT);
-        } else {
+            // adds the tile in tensor memory (its O columns, in units of 2^m_tile / kWUnit) to o
+            auto add_tile = [&]() {
+                int c[kOCols3];
+                tmem_load<kOCols3>(tlane + Sh::kOCol + 3 * par0, c);
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const float f = fmaf((float)c[3 * g], 65536.f, (float)(c[3 * g + 1] * 256 + c[3 * g + 2]));
+                    if (m_tile[g] > m_o[g]) {  // the same in every thread of the warp
+                        o[g] = o[g] * fast_exp2(m_o[g] - m_tile[g]) + f;
+                        m_o[g] = m_tile[g];
+                    } else if (m_tile[g] > -INFINITY) {
+                        o[g] = fmaf(f, fast_exp2(m_tile[g] - m_o[g]), o[g]);
+                    }
+                }
+            };
+            for (int j = 0; j < ntiles; ++j, ++t) {
+                float *wm = wmax + (t & 1) * 4 * kV;
+                sound = __all_sync(0xffffffffu, sound && mbar_wait(s_full + (t & 1), (t >> 1) & 1) && !*abort_flag);
+                float x[kV];  // log2 of the weight
+                if (sound) {
+                    fence_after();
+                    const Scales &sc = scales[t % kScales];
+                    const float ks = sc.k[block], vs = sc.v[block];
+                    const bool valid = (sc.valid >> block) & 1u;
+                    const float lv = vs > 0.f ? log2f(vs) : -INFINITY;
+                    const int tok = first + j * kTok + r * kPar;
+                    int c[kCols3];
+                    tmem_load<kCols3>(tlane + Sh::kSCol + (t & 1) * kN, c);
+#pragma unroll
+                    for (int v = 0; v < kV; ++v) {
+                        const float f = fmaf((float)c[3 * v], 65536.f, (float)(c[3 * v + 1] * 256 + c[3 * v + 2]));
+                        const float score = f * (qs[v] * ks);
+                        const bool live = valid && tok + v / G < L;
+                        if (live) {
+                            const float d = score - m_l[v];
+                            const float e = fast_exp2(-fabsf(d));
+                            l[v] = d > 0.f ? fmaf(l[v], e, 1.f) : l[v] + e;
+                            m_l[v] = fmaxf(m_l[v], score);
+                        }
+                        x[v] = live ? score + lv : -INFINITY;
+                    }
+                    // the tile's largest weight per head, over this warp
+#pragma unroll
+                    for (int v = 0; v < kV; ++v) {
+                        const float mw = warp_max(x[v]);
+                        if (lane == 0) wm[warp * kV + v] = mw;
+                    }
+                }
+                ok = softmax_sync_and(sound);
+                if (!ok) break;
+                float mt[kV];
+#pragma unroll
+                for (int v = 0; v < kV; ++v)
+                    mt[v] = fmaxf(fmaxf(wm[v], wm[kV + v]), fmaxf(wm[2 * kV + v], wm[3 * kV + v]));
+                if (j > 0) {  // O of the tile before is there: P and O are free once it is added up
+                    sound = __all_sync(0xffffffffu, mbar_wait(o_full, (t - 1) & 1) && !*abort_flag);
+                    if (!sound) continue;  // (the next barrier tells the others)
+                    fence_after();
+                    add_tile();
+                }
+#pragma unroll
+                for (int g = 0; g < G; ++g) m_tile[g] = kPar == 2 && par0 ? mt[kV - G + g] : mt[g];
+                // ---- the weights' digits, row 3 v + i, byte r of the row (its 16-byte chunks swizzled)
+#pragma unroll
+                for (int v = 0; v < kV; ++v) {
+                    const float w = x[v] > -INFINITY ? fast_exp2(x[v] - mt[v]) : 0.f;
+                    const unsigned u = __float2uint_rn(w * kWUnit);
+                    const int d = 3 * v;
+                    Ps[d * kRowBytes + (r ^ ((d & 7) << 4))] = (unsigned char)(u >> 16);
+                    Ps[(d + 1) * kRowBytes + (r ^ (((d + 1) & 7) << 4))] = (unsigned char)(u >> 8);
+                    Ps[(d + 2) * kRowBytes + (r ^ (((d + 2) & 7) << 4))] = (unsigned char)u;
+                }
+                fence_proxy_async_smem();
+                fence_before();
+                mbar_arrive(p_full);
+            }
+            if (!ok) break;
+            if (ntiles > 0) {
+                sound = __all_sync(0xffffffffu, sound && mbar_wait(o_full, (t - 1) & 1) && !*abort_flag);
+                if (sound) {
+                    fence_after();
+                    add_tile();
+                }
+                ok = softmax_sync_and(sound);
+                if (!ok) break;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(i_empty + slot);
+            // ---- the threads' sums, where the weights' digits were (their product is done), and the output
 #pragma unroll
             for (int v = 0; v < kV; ++v) {
                 const float mw = warp_max(m_l[v]);
@@ -556,18 +773,18 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
                 if (kPar == 2 && r >= D) red_o[g * D + r - D] = o[g];
             }
             if constexpr (kPar == 2) named_bar_sync(1, kSoftmaxThreads);
-            if (r < D) {
+            if (r < D && write) {
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     if (g >= g_valid) continue;
                     if constexpr (kPar == 2) o[g] += red_o[g * D + r];
                     const size_t row = row0 + g;
                     if (p.partition_size) {
-                        const size_t slot = row * p.max_parts + blockIdx.x;
-                        p.ws_acc[slot * D + r] = o[g] * (1.f / kWUnit);
+                        const size_t at = row * p.max_parts + part;
+                        p.ws_acc[at * D + r] = o[g] * (1.f / kWUnit);
                         if (r == 0) {
-                            p.ws_ml[slot * 2] = m[g];  // log2 units
-                            p.ws_ml[slot * 2 + 1] = sum[g];
+                            p.ws_ml[at * 2] = m[g];  // log2 units
+                            p.ws_ml[at * 2 + 1] = sum[g];
                         }
                     } else {
                         const float y = sum[g] != 0.f ? o[g] / (sum[g] * kWUnit) : 0.f;
@@ -575,7 +792,9 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
                     }
                 }
             }
+            // (the sums are read before the next weights are written: the next item's first barrier is in between)
         }
+        if (!ok && r == 0) give_up();
     }
     fence_before();
     __syncthreads();
@@ -651,14 +870,25 @@ template <int D> __global__ void __launch_bounds__(128) join_kernel(const Decode
 }
 
 template <typename T, int D, int G>
-static cudaError_t launch_decode_t(const CUtensorMap &km, const CUtensorMap &vm, const DecodeParams &p,
-                                   cudaStream_t stream) {
+static cudaError_t launch_decode_t(const CUtensorMap &km, const CUtensorMap &vm, DecodeParams p, cudaStream_t stream) {
+    using Sh = Shape<G * (128 / D)>;
     auto kern = decode_kernel<T, D, G>;
-    constexpr int kSmem = Shape<G * (128 / D)>::kSmemBytes;
     static AttrCache attr;
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmem, &attr);
+    static std::atomic<int> regs{0};
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), Sh::kSmemBytes, &attr);
     if (e != cudaSuccess) return e;
-    kern<<<dim3(p.max_parts, p.num_kv_heads * p.sub_groups, p.num_seqs), kThreads, kSmem, stream>>>(km, vm, p);
+    if (regs.load(std::memory_order_relaxed) == 0) {
+        cudaFuncAttributes at;
+        e = cudaFuncGetAttributes(&at, reinterpret_cast<const void *>(kern));
+        if (e != cudaSuccess) return e;
+        // a launch with fewer registers than are taken over would wait for them for good
+        if (at.numRegs != Sh::kRegs) return cudaErrorInvalidConfiguration;
+        regs.store(at.numRegs, std::memory_order_relaxed);
+    }
+    const dim3 grid(p.max_parts, p.num_kv_heads * p.sub_groups, p.num_seqs);
+    // blocks that all start at once leave none to take over
+    p.steal = (long long)grid.x * grid.y * grid.z > (long long)Sh::kCtas * sm_count();
+    kern<<<grid, kThreads, Sh::kSmemBytes, stream>>>(km, vm, p);
     return cudaGetLastError();
 }
 

@@ -430,6 +430,34 @@ def test_decode_bad_tables_and_lengths(pa):
     assert not any(torch.isnan(x).any() for x in (out[0], out[3]))
 
 
+@pytest.mark.parametrize("D,bs,Hq,Hkv", [(128, 16, 2, 2), (128, 32, 16, 2), (64, 16, 2, 2), (64, 32, 8, 1), (64, 16, 4, 1)])
+def test_decode_more_items_than_ctas(pa, D, bs, Hq, Hkv):
+    """More (sequence, kv head) pairs than fit the GPU at once, so each CTA
+    works through several: lengths of 0, 1, a few tiles and around their ends."""
+    rng = np.random.default_rng(D + Hq)
+    lens = rng.integers(0, 400, 900)
+    lens[rng.integers(0, 900, 200)] = rng.choice([0, 1, 16, 128, 129, 256, 257, 512, 513, 1000], 200)
+    c = Case(Hq, Hkv, D, bs, lens, seed=77, MB=64)
+    order = rng.permutation(900)
+    a = c.run(pa, torch.bfloat16, order=order)
+    assert pa.pa_read_device_errors() == 0
+    c.check(a, torch.bfloat16)
+    assert torch.equal(a, c.run(pa, torch.bfloat16, workspace=False))
+    assert (a[torch.from_numpy(lens == 0).cuda()] == 0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_non_finite_query_gives_nan_rows_only_there(pa, D):
+    c = Case(4, 2, D, 16, [300, 0, 40], seed=39)
+    c.q[0, 1, 3], c.q[2, 2, 0], c.q[1, 0, 0] = math.nan, math.inf, math.nan
+    for ws in (True, False):
+        out = c.run(pa, torch.float16, workspace=ws)
+        bad = torch.zeros(out.shape[:2], dtype=torch.bool, device="cuda")
+        bad[0, 1] = bad[2, 2] = True
+        assert torch.isnan(out[bad]).all() and torch.isfinite(out[~bad]).all()
+        assert (out[1] == 0).all()
+
+
 def test_decode_empty_batches(pa):
     c = Case(4, 2, 128, 16, [0, 0], seed=37)
     assert (c.run(pa, torch.float16) == 0).all()
