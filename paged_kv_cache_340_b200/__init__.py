@@ -159,7 +159,9 @@ class _Library:
     def __getattr__(self, name):
         if _Library._cdll is None:
             _Library._cdll = _load()
-        return getattr(_Library._cdll, name)
+        fn = getattr(_Library._cdll, name)
+        setattr(self, name, fn)  # found without this call from now on
+        return fn
 
 
 _lib = _Library()
@@ -184,15 +186,19 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return t.data_ptr()
 
 
-def _expect(dtype: torch.dtype, *tensors: Optional[torch.Tensor]) -> None:
-    for t in tensors:
-        if t is not None and t.dtype != dtype:
-            raise ValueError(f"expected a {dtype} tensor, got {t.dtype}")
+def _addr(t: torch.Tensor, dtype: torch.dtype, device: int) -> int:
+    """Address of a contiguous tensor of the type on the device (the current
+    one: its stream is the call's)."""
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"expected a contiguous {dtype} tensor on cuda:{device}, got {t.dtype} on {t.device} "
+                         f"of shape {tuple(t.shape)} and strides {t.stride()}")
+    return t.data_ptr()
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream without the Stream object (0.3 us instead of 3.3)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -467,29 +473,28 @@ def pa_dpool_append(pool: DevicePool, block_tables, context_lens, new_lens, q_st
     length in block_tables [S, MB] and context_lens [S], q_start [S + 1],
     slots in slot_mapping [max_tokens] (then -1), pairs to copy in cow_pairs
     [S, 2] int64 and their number in num_cow [1] (all on the device; see pa.h)."""
-    S = context_lens.shape[0]
-    if new_lens.shape[0] != S or block_tables.shape[0] != S or q_start.shape[0] != S + 1 or cow_pairs.shape[0] != S:
+    S, MB = block_tables.shape
+    if context_lens.shape != (S,) or new_lens.shape != (S,) or q_start.shape != (S + 1,) or cow_pairs.shape != (S, 2):
         raise ValueError("pa_dpool_append: one row, length and pair per sequence, and one more q_start")
-    _expect(torch.int32, pool.state, block_tables, context_lens, new_lens, q_start, slot_mapping, num_cow)
-    _expect(torch.int64, cow_pairs)
-    T = slot_mapping.shape[0]
-    rc = _lib.pa_dpool_append(_ptr(pool.state), pool.num_blocks, pool.block_size, _ptr(block_tables) if S else None,
-                              block_tables.shape[1], _ptr(context_lens) if S else None, _ptr(new_lens) if S else None,
-                              S, _ptr(q_start), _ptr(slot_mapping) if T else None, T, _ptr(cow_pairs) if S else None,
-                              _ptr(num_cow), _stream(stream))
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    rc = _lib.pa_dpool_append(_addr(pool.state, i32, dev), pool.num_blocks, pool.block_size,
+                              _addr(block_tables, i32, dev), MB, _addr(context_lens, i32, dev),
+                              _addr(new_lens, i32, dev), S, _addr(q_start, i32, dev), _addr(slot_mapping, i32, dev),
+                              slot_mapping.shape[0], _addr(cow_pairs, torch.int64, dev), _addr(num_cow, i32, dev),
+                              _stream(stream))
     _check(rc, "pa_dpool_append")
 
 
 def pa_dpool_release(pool: DevicePool, block_tables, context_lens, finished, stream=None) -> None:
     """Returns the blocks of every sequence s with finished[s] != 0 (device
     int32 [S]); its table entries become -1 and its length 0."""
-    S = context_lens.shape[0]
-    if finished.shape[0] != S or block_tables.shape[0] != S:
+    S, MB = block_tables.shape
+    if context_lens.shape != (S,) or finished.shape != (S,):
         raise ValueError("pa_dpool_release: one row, length and mark per sequence")
-    _expect(torch.int32, pool.state, block_tables, context_lens, finished)
-    rc = _lib.pa_dpool_release(_ptr(pool.state), pool.num_blocks, pool.block_size, _ptr(block_tables) if S else None,
-                               block_tables.shape[1], _ptr(context_lens) if S else None, _ptr(finished) if S else None,
-                               S, _stream(stream))
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    rc = _lib.pa_dpool_release(_addr(pool.state, i32, dev), pool.num_blocks, pool.block_size,
+                               _addr(block_tables, i32, dev), MB, _addr(context_lens, i32, dev),
+                               _addr(finished, i32, dev), S, _stream(stream))
     _check(rc, "pa_dpool_release")
 
 
@@ -497,11 +502,11 @@ def pa_dpool_release(pool: DevicePool, block_tables, context_lens, finished, str
 # k_cache/v_cache int8 [NB, Hkv, bs, D]; k_scale/v_scale float32 [NB, Hkv].
 
 def _q8b_cache(k_cache, v_cache, k_scale, v_scale):
-    _expect(torch.int8, k_cache, v_cache)
-    _expect(torch.float32, k_scale, v_scale)
-    if v_cache.shape != k_cache.shape or k_scale.shape != k_cache.shape[:2] or v_scale.shape != k_cache.shape[:2]:
+    shape = k_cache.shape
+    NB, Hkv, _, _ = shape
+    if v_cache.shape != shape or k_scale.shape != (NB, Hkv) or v_scale.shape != (NB, Hkv):
         raise ValueError("expected k_cache and v_cache [NB, Hkv, bs, D] with k_scale and v_scale [NB, Hkv]")
-    return k_cache.shape
+    return shape
 
 
 def pa_append_q8b(key, value, q_start, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
@@ -509,15 +514,17 @@ def pa_append_q8b(key, value, q_start, k_cache, v_cache, k_scale, v_scale, block
     """Writes rows q_start[s] .. q_start[s+1]-1 of key and value [T, Hkv, D] as
     the last tokens of sequence s, quantized with one scale per (block, head)."""
     NB, Hkv, bs, D = _q8b_cache(k_cache, v_cache, k_scale, v_scale)
-    S, T = context_lens.shape[0], key.shape[0]
-    if key.dtype != value.dtype or key.shape != (T, Hkv, D) or value.shape != key.shape:
-        raise ValueError("pa_append_q8b: key and value are [T, Hkv, D] of one type")
-    if q_start.shape[0] != S + 1 or block_tables.shape[0] != S:
-        raise ValueError("pa_append_q8b: one table row per sequence, and one more q_start")
-    _expect(torch.int32, q_start, block_tables, context_lens)
-    rc = _lib.pa_append_q8b(_ptr(key), _ptr(value), _dtype(key), _ptr(q_start), T, _ptr(k_cache), _ptr(v_cache),
-                            _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1],
-                            _ptr(context_lens), S, NB, Hkv, D, bs, _stream(stream))
+    T = key.shape[0]
+    S, MB = block_tables.shape
+    if key.shape != (T, Hkv, D) or value.shape != (T, Hkv, D):
+        raise ValueError("pa_append_q8b: key and value are [T, Hkv, D]")
+    if q_start.shape != (S + 1,) or context_lens.shape != (S,):
+        raise ValueError("pa_append_q8b: one table row and length per sequence, and one more q_start")
+    dev, i8, i32, f32, src = torch.cuda.current_device(), torch.int8, torch.int32, torch.float32, key.dtype
+    rc = _lib.pa_append_q8b(_addr(key, src, dev), _addr(value, src, dev), _dtype(key), _addr(q_start, i32, dev), T,
+                            _addr(k_cache, i8, dev), _addr(v_cache, i8, dev), _addr(k_scale, f32, dev),
+                            _addr(v_scale, f32, dev), _addr(block_tables, i32, dev), MB,
+                            _addr(context_lens, i32, dev), S, NB, Hkv, D, bs, _stream(stream))
     _check(rc, "pa_append_q8b")
 
 
@@ -532,16 +539,25 @@ def pa_decode_q8b(out, query, k_cache, v_cache, k_scale, v_scale, block_tables, 
     their tokens."""
     NB, Hkv, bs, Dk = _q8b_cache(k_cache, v_cache, k_scale, v_scale)
     S, Hq, D = query.shape
-    if Dk != D or out.shape != query.shape or context_lens.shape[0] != S or block_tables.shape[0] != S:
+    MB = block_tables.shape[1]
+    if Dk != D or out.shape != (S, Hq, D) or context_lens.shape != (S,) or block_tables.shape != (S, MB):
         raise ValueError("pa_decode_q8b: query and out [S, Hq, D], one table row and length per sequence")
-    _expect(torch.int32, block_tables, context_lens, seq_order)
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    if workspace is not None and nbytes == 0:
-        _check(PA_ERR_WORKSPACE, "pa_decode_q8b")  # an empty tensor has no address: not "no workspace"
-    rc = _lib.pa_decode_q8b(_ptr(out), _ptr(query), _dtype(query), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-                            _ptr(v_scale), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), S, Hq, Hkv,
-                            D, float(scale), bs, NB, int(max_context_len), _dtype(out), _ptr(seq_order),
-                            _ptr(workspace), nbytes, _stream(stream))
+    dev, i8, i32, f32 = torch.cuda.current_device(), torch.int8, torch.int32, torch.float32
+    ws = order = None
+    nbytes = 0
+    if workspace is not None:
+        ws, nbytes = _addr(workspace, workspace.dtype, dev), workspace.nbytes
+        if nbytes == 0:
+            _check(PA_ERR_WORKSPACE, "pa_decode_q8b")  # an empty tensor has no address: not "no workspace"
+    if seq_order is not None:
+        if seq_order.shape != (S,):
+            raise ValueError("pa_decode_q8b: seq_order has one entry per sequence")
+        order = _addr(seq_order, i32, dev)
+    rc = _lib.pa_decode_q8b(_addr(out, out.dtype, dev), _addr(query, query.dtype, dev), _dtype(query),
+                            _addr(k_cache, i8, dev), _addr(v_cache, i8, dev), _addr(k_scale, f32, dev),
+                            _addr(v_scale, f32, dev), _addr(block_tables, i32, dev), MB,
+                            _addr(context_lens, i32, dev), S, Hq, Hkv, D, scale, bs, NB, max_context_len, _dtype(out),
+                            order, ws, nbytes, _stream(stream))
     _check(rc, "pa_decode_q8b")
 
 
@@ -549,11 +565,13 @@ def pa_copy_blocks_q8b(k_cache, v_cache, k_scale, v_scale, src_dst_pairs, num_pa
     """pa_copy_blocks of codes and scales; with num_pairs (a device int32) only
     that many of the pairs."""
     NB, Hkv, bs, D = _q8b_cache(k_cache, v_cache, k_scale, v_scale)
-    n = src_dst_pairs.shape[0] if src_dst_pairs is not None else 0
-    _expect(torch.int64, src_dst_pairs)
-    _expect(torch.int32, num_pairs)
-    rc = _lib.pa_copy_blocks_q8b(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                                 _ptr(src_dst_pairs) if n else None, _ptr(num_pairs), n, NB, Hkv, D, bs,
+    n = src_dst_pairs.shape[0]
+    if src_dst_pairs.shape != (n, 2):
+        raise ValueError("pa_copy_blocks_q8b: src_dst_pairs is [n, 2]")
+    dev, i8, f32 = torch.cuda.current_device(), torch.int8, torch.float32
+    rc = _lib.pa_copy_blocks_q8b(_addr(k_cache, i8, dev), _addr(v_cache, i8, dev), _addr(k_scale, f32, dev),
+                                 _addr(v_scale, f32, dev), _addr(src_dst_pairs, torch.int64, dev),
+                                 None if num_pairs is None else _addr(num_pairs, torch.int32, dev), n, NB, Hkv, D, bs,
                                  _stream(stream))
     _check(rc, "pa_copy_blocks_q8b")
 

@@ -90,6 +90,7 @@ constexpr int kTile = 128 * kRowBytes;         // 16 KB of K or V
 constexpr int kStages = 2;
 constexpr int kItems = 2;                      // items known ahead, the current one included
 constexpr int kScales = 4;                     // tiles whose scales are kept: warp 5 is at most three tiles ahead
+constexpr int kClaimAhead = 4;                 // tiles of an item still to be loaded when the next one is claimed
 constexpr int kMaxBlocks = 16;                 // blocks of a tile, at most
 constexpr int kSoftmaxThreads = 128;
 constexpr int kMmaWarp = 4, kLoadK = 5, kLoadV = 6, kItemWarp = 7;
@@ -389,21 +390,22 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
                         raw[g] = __ldg(reinterpret_cast<const Raw *>(static_cast<const T *>(p.query) +
                                                                      ((size_t)s * p.num_heads + head0 + g) * D) + lane);
                 }
+                const int first = x * p.partition_size;
+                const int lb = (first >> bs_shift) + lane;
+                int id = lane < blocks && lb < p.max_blocks ? __ldg(p.tables + (size_t)s * p.max_blocks + lb) : -1;
                 int L = __ldg(p.ctx + s);
                 const int room = (int)min((long long)p.max_blocks << bs_shift, (long long)p.max_ctx);
                 if (write && (L < 0 || L > room)) {
                     if (lane == 0) record_error(p.err, PA_DEVERR_CONTEXT);
                     L = L < 0 ? 0 : room;
                 }
-                const int first = x * p.partition_size;
                 if (p.partition_size) {
                     L = min(L, first + p.partition_size);
                     if (first >= L) write = 0;  // no such partition: its entry is not read
                 }
                 if (!write) L = first;
                 const int ntiles = L > first ? (L - first + kTok - 1) / kTok : 0;
-                const int lb = (first >> bs_shift) + lane, nblk = (L + (1 << bs_shift) - 1) >> bs_shift;
-                const int id = ntiles && lane < blocks && lb < nblk ? __ldg(p.tables + (size_t)s * p.max_blocks + lb) : -1;
+                if (lb >= (L + (1 << bs_shift) - 1) >> bs_shift) id = -1;
                 if (lane < kMaxBlocks) it.ids[lane] = id;
                 if (lane == 0) {
                     it.ntiles = ntiles;
@@ -504,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(i_empty + slot);
-                    if (!is_v && p.steal && ntiles < 4) mbar_arrive(claim);
+                    if (!is_v && p.steal && ntiles < kClaimAhead) mbar_arrive(claim);
                 }
                 auto look = [&](int j) -> int {
                     const int lb = b0 + j * blocks + lane;
@@ -541,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
                         __syncwarp();
                         if (lane == 0) {
                             mbar_arrive(full + b);
-                            if (p.steal && ntiles >= 4 && j == ntiles - 4) mbar_arrive(claim);
+                            if (p.steal && ntiles >= kClaimAhead && j == ntiles - kClaimAhead) mbar_arrive(claim);
                         }
                     }
                     id = id_next;

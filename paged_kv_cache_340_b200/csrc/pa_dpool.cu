@@ -36,9 +36,16 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCluster = 8;  // the largest portable cluster
-constexpr int kPer = PA_DPOOL_MAX_SEQS / kThreads;  // sequences per thread, at most
-static_assert(kPer * kThreads == PA_DPOOL_MAX_SEQS, "a thread holds a run of whole sequences");
+// CTAs of the cluster: 8 is the largest portable size; where a call may have
+// enough to do for more, 16.
+constexpr int kCluster = 8, kClusterLarge = 16;
+constexpr int kBatch = 8;    // items of a warp whose accesses are in flight at once
+constexpr int kClaimed = INT32_MIN;  // the count of a block that release_kernel is freeing
+// The kernels are compiled for at most kPer sequences a thread, in registers:
+// one, for up to 1024 sequences, and as many as PA_DPOOL_MAX_SEQS needs (whose
+// registers spill).
+constexpr int kPerMost = PA_DPOOL_MAX_SEQS / kThreads;
+static_assert(kPerMost * kThreads == PA_DPOOL_MAX_SEQS, "a thread holds a run of whole sequences");
 
 struct AppendParams {
     int32_t *state;
@@ -71,10 +78,16 @@ struct ReleaseParams {
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return a / b + (a % b != 0); }
 
-// Whether `state` is a sound pool of these sizes.
-__device__ __forceinline__ bool header_ok(const Pool &p, int nb, int bs) {
-    return __ldcg(p.hdr + 5) == kMagic && __ldcg(p.hdr) == nb && __ldcg(p.hdr + 1) == bs;
-}
+struct Header {
+    int nb, bs, policy, head, count, magic;
+    __device__ __forceinline__ explicit Header(const Pool &p)
+        : nb(__ldcg(p.hdr)), bs(__ldcg(p.hdr + 1)), policy(__ldcg(p.hdr + 2)), head(__ldcg(p.hdr + 3)),
+          count(__ldcg(p.hdr + 4)), magic(__ldcg(p.hdr + 5)) {}
+    // whether the state is a sound pool of these sizes
+    __device__ __forceinline__ bool ok(int num_blocks, int block_size) const {
+        return magic == kMagic && nb == num_blocks && bs == block_size;
+    }
+};
 
 template <typename T> __device__ __forceinline__ T warp_inclusive(T v, int lane) {
 #pragma unroll
@@ -85,21 +98,46 @@ template <typename T> __device__ __forceinline__ T warp_inclusive(T v, int lane)
     return v;
 }
 
-// Exclusive scan of one value per thread over the CTA; *total receives the
-// sum. `sums` holds kWarps + 1 values; the call ends with a CTA barrier.
-template <typename T> __device__ T block_exclusive(T v, T *sums, T *total) {
+// Exclusive scans of two values per thread over the CTA, in place; *ta and *tb
+// receive the sums. `sums` holds 2 (kWarps + 1) values; the call ends with a
+// CTA barrier.
+__device__ __forceinline__ void block_exclusive2(long long &a, long long &b, long long *sums, long long *ta,
+                                                 long long *tb) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const T inc = warp_inclusive(v, lane);
+    long long *sa = sums, *sb = sums + kWarps + 1;
+    const long long ia = warp_inclusive(a, lane), ib = warp_inclusive(b, lane);
+    if (lane == 31) {
+        sa[warp] = ia;
+        sb[warp] = ib;
+    }
+    __syncthreads();
+    if (warp < 2) {
+        long long *x = warp == 0 ? sa : sb;
+        const long long w = x[lane], wi = warp_inclusive(w, lane);
+        x[lane] = wi - w;
+        if (lane == 31) x[kWarps] = wi;
+    }
+    __syncthreads();
+    a = sa[warp] + ia - a;
+    b = sb[warp] + ib - b;
+    *ta = sa[kWarps];
+    *tb = sb[kWarps];
+    __syncthreads();
+}
+
+// The same of one value, returned.
+__device__ __forceinline__ int block_exclusive(int v, int *sums, int *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int inc = warp_inclusive(v, lane);
     if (lane == 31) sums[warp] = inc;
     __syncthreads();
     if (warp == 0) {
-        const T w = sums[lane];
-        const T wi = warp_inclusive(w, lane);
+        const int w = sums[lane], wi = warp_inclusive(w, lane);
         sums[lane] = wi - w;
         if (lane == 31) sums[kWarps] = wi;
     }
     __syncthreads();
-    const T r = sums[warp] + inc - v;
+    const int r = sums[warp] + inc - v;
     *total = sums[kWarps];
     __syncthreads();
     return r;
@@ -118,7 +156,7 @@ __device__ __forceinline__ int find_run(const int *pre, int n, int k) {
 
 // ------------------------------------------------------------------ append
 
-__global__ void __launch_bounds__(kThreads, 1) append_kernel(const AppendParams q) {
+template <int kPer> __global__ void __launch_bounds__(kThreads, 1) append_kernel(const AppendParams q) {
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
     const int tid = threadIdx.x;
@@ -132,9 +170,21 @@ __global__ void __launch_bounds__(kThreads, 1) append_kernel(const AppendParams 
     int *tok_pre = dyn;                  // [S + 1] new tokens before sequence s
     int *take_pre = tok_pre + S + 1;     // [S + 1] blocks taken before sequence s
     int *ctx_cow = take_pre + S + 1;     // [S] context length, sign bit: its last block is copied
-    __shared__ long long sums[kWarps + 1];
+    __shared__ long long sums[2 * (kWarps + 1)];
 
     const Pool p = views(q.state, nb);
+    const Header hdr(p);
+    const int per = (S + kThreads - 1) / kThreads;
+    const int s0 = tid * per, s1 = min(S, s0 + per);
+    int ctx[kPer], nw[kPer], blk[kPer], ref[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {  // in flight with the header
+        ctx[i] = nw[i] = 0;
+        if (s0 + i < s1) {
+            ctx[i] = __ldcg(q.ctx + s0 + i);
+            nw[i] = __ldg(q.new_lens + s0 + i);
+        }
+    }
     int bad = 0;  // PA_DEVERR_* bits
     auto refuse = [&]() {  // nothing is applied: outputs that make the step's other calls do nothing
         for (int i = gtid; i <= S; i += gstep) q.q_start[i] = 0;
@@ -142,73 +192,64 @@ __global__ void __launch_bounds__(kThreads, 1) append_kernel(const AppendParams 
         for (int i = gtid; i < 2 * S; i += gstep) q.cow_pairs[i] = -1;
         if (gtid == 0) *q.num_cow = 0;
     };
-    if (!header_ok(p, nb, bs)) {  // the same in every CTA: the header changes behind the cluster's barriers
+    if (!hdr.ok(nb, bs)) {  // the same in every CTA: the header changes behind the cluster's barriers
         if (gtid == 0) record_error(q.err, PA_DEVERR_POOL);
         refuse();
         return;
     }
-    const int policy = __ldcg(p.hdr + 2), head = __ldcg(p.hdr + 3), count = __ldcg(p.hdr + 4);
+    const int head = hdr.head, count = hdr.count;
 
-    // ---- lengths, and who writes into which partly filled block
-    const int per = (S + kThreads - 1) / kThreads;
-    const int s0 = tid * per, s1 = min(S, s0 + per);
-    int ctx[kPer], nw[kPer], blk[kPer];
+    // ---- who writes into which partly filled block
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int s = s0 + i;
-        ctx[i] = nw[i] = 0;
         blk[i] = -1;
-        if (s >= s1) continue;
-        const int c = __ldcg(q.ctx + s), n = __ldg(q.new_lens + s);
-        if (c < 0 || n < 0 || c > (long long)MB * bs) {
+        if (ctx[i] < 0 || nw[i] < 0 || ctx[i] > (long long)MB * bs) {
             bad |= PA_DEVERR_CONTEXT;
-            continue;
-        }
-        if ((long long)c + n > (long long)MB * bs) {
+            ctx[i] = nw[i] = 0;
+        } else if ((long long)ctx[i] + nw[i] > (long long)MB * bs) {
             bad |= PA_DEVERR_POOL;
-            continue;
-        }
-        ctx[i] = c;
-        nw[i] = n;
-        if (n > 0 && c % bs != 0) {
-            const int b = __ldcg(q.tables + (size_t)s * MB + c / bs);
-            if (b < 0 || b >= nb) {
+            ctx[i] = nw[i] = 0;
+        } else if (nw[i] > 0 && ctx[i] % bs != 0) {
+            blk[i] = __ldcg(q.tables + (size_t)(s0 + i) * MB + ctx[i] / bs);
+            if (blk[i] < 0 || blk[i] >= nb) {
                 bad |= PA_DEVERR_BLOCK_ID;
-                continue;
+                blk[i] = -1;
             }
-            if (__ldcg(p.ref + b) < 1) {
-                bad |= PA_DEVERR_POOL;
-                continue;
-            }
-            blk[i] = b;
-            if (mine) {
-                atomicAdd(p.writers + b, 1);
-                atomicMax(p.last_writer + b, s);
-            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) ref[i] = blk[i] >= 0 ? __ldcg(p.ref + blk[i]) : 1;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (ref[i] < 1) bad |= PA_DEVERR_POOL;
+        if (ref[i] <= 1) {
+            blk[i] = -1;  // this sequence's alone: written in place
+        } else if (mine) {
+            atomicAdd(p.writers + blk[i], 1);
+            atomicMax(p.last_writer + blk[i], s0 + i);
         }
     }
     cluster.sync();
 
     // ---- takes and their places; the same in every CTA
-    long long tok = 0;
+    long long tok_at = 0;
     int takes = 0, cows = 0;
     bool cow[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         cow[i] = false;
         if (blk[i] >= 0) {
-            const int r = __ldcg(p.ref + blk[i]), w = __ldcg(p.writers + blk[i]);
-            if (w > r) bad |= PA_DEVERR_POOL;  // more tables hold the block than its count says
-            cow[i] = r > 1 && !(w == r && __ldcg(p.last_writer + blk[i]) == s0 + i);
+            const int w = __ldcg(p.writers + blk[i]), last = __ldcg(p.last_writer + blk[i]);
+            if (w > ref[i]) bad |= PA_DEVERR_POOL;  // more tables hold the block than its count says
+            cow[i] = !(w == ref[i] && last == s0 + i);
         }
-        tok += nw[i];
+        tok_at += nw[i];
         takes += (int)cow[i] + ceil_div(ctx[i] + nw[i], bs) - ceil_div(ctx[i], bs);
         cows += cow[i];
     }
     // takes and cows are below 2^30 (sequences x table entries): one 64-bit scan for both
-    long long all_tok, all_tc;
-    long long tok_at = block_exclusive<long long>(tok, sums, &all_tok);
-    const long long tc_at = block_exclusive<long long>(((long long)takes << 32) | (unsigned)cows, sums, &all_tc);
+    long long tc_at = ((long long)takes << 32) | (unsigned)cows, all_tok, all_tc;
+    block_exclusive2(tok_at, tc_at, sums, &all_tok, &all_tc);
     int take_at = (int)(tc_at >> 32), cow_at = (int)(unsigned)tc_at;
     const int all_takes = (int)(all_tc >> 32), all_cows = (int)(unsigned)all_tc;
     if (all_tok > q.max_tokens || all_takes > count) bad |= PA_DEVERR_POOL;
@@ -245,10 +286,9 @@ __global__ void __launch_bounds__(kThreads, 1) append_kernel(const AppendParams 
     }
 
     // ---- apply. Block k of the step's takes:
-    const long long first = policy == PA_POOL_FIFO ? head : (long long)head + count - 1;
     auto block_of = [&](int k) -> int {
-        const long long at = policy == PA_POOL_FIFO ? first + k : first - k;
-        return __ldcg(p.ring + at % nb);
+        const int at = hdr.policy == PA_POOL_FIFO ? head + k : head + count - 1 - k;  // from 0 to below 2 nb
+        return __ldcg(p.ring + (at < nb ? at : at - nb));
     };
     if (mine) {
         int t = (int)tok_at, k = take_at;
@@ -260,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) append_kernel(const AppendParams 
             q.ctx[s] = ctx[i] + nw[i];
             if (cow[i]) {
                 const int id = block_of(k);
-                atomicSub(p.ref + blk[i], 1);
+                atomicSub(p.ref + blk[i], 1);  // other sequences of the call may copy it too
                 reinterpret_cast<longlong2 *>(q.cow_pairs)[cow_at] = make_longlong2(blk[i], id);
                 ++cow_at;
             }
@@ -279,32 +319,63 @@ __global__ void __launch_bounds__(kThreads, 1) append_kernel(const AppendParams 
         q.tables[(size_t)s * MB + j] = id;
         p.ref[id] = 1;
     }
-    for (int t = gtid; t < q.max_tokens; t += gstep) {
-        int slot = -1;
-        if (t < all_tok) {
-            const int s = find_run(tok_pre, S, t);
-            const int c = ctx_cow[s] & 0x7fffffff, cw = ctx_cow[s] < 0;
-            const int pos = c + t - tok_pre[s];
-            const int j = pos / bs, have = ceil_div(c, bs);
-            int id;
-            if (j >= have) id = block_of(take_pre[s] + cw + j - have);
-            else if (cw) id = block_of(take_pre[s]);
-            else id = __ldcg(q.tables + (size_t)s * MB + j);  // kept: no thread writes this entry
-            slot = id * bs + (pos - j * bs);
+    // Slots, four consecutive tokens a thread: one search and, within a block,
+    // one look at the list serve all four (a token a thread took 2.6 times as
+    // long for 256 prompts of 262,000 tokens).
+    const bool vec = (reinterpret_cast<uintptr_t>(q.slots) & 15) == 0;
+    const int quads = (q.max_tokens + 3) / 4;
+#pragma unroll 2
+    for (int i = gtid; i < quads; i += gstep) {
+        int v[4] = {-1, -1, -1, -1};
+        int s = -1, next = 4 * i, j = 0, o = 0, id = 0;  // sequence, its end, block and offset of the token, block id
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int t = 4 * i + u;
+            if (t >= all_tok) continue;
+            bool look = true;
+            if (t >= next) {  // the first token here, or of a new sequence
+                if (s < 0) s = find_run(tok_pre, S, t);
+                else
+                    do ++s;
+                    while (t >= tok_pre[s + 1]);
+                next = tok_pre[s + 1];
+                const int pos = (ctx_cow[s] & 0x7fffffff) + t - tok_pre[s];
+                j = pos / bs;
+                o = pos - j * bs;
+            } else if (++o == bs) {
+                o = 0;
+                ++j;
+            } else {
+                look = false;
+            }
+            if (look) {
+                const int c = ctx_cow[s] & 0x7fffffff, cw = ctx_cow[s] < 0;
+                const int have = ceil_div(c, bs);
+                if (j >= have) id = block_of(take_pre[s] + cw + j - have);
+                else if (cw) id = block_of(take_pre[s]);
+                else id = __ldcg(q.tables + (size_t)s * MB + j);  // kept: no thread writes this entry
+            }
+            v[u] = id * bs + o;
         }
-        q.slots[t] = slot;
+        if (vec && 4 * i + 3 < q.max_tokens) {
+            reinterpret_cast<int4 *>(q.slots)[i] = make_int4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (4 * i + u < q.max_tokens) q.slots[4 * i + u] = v[u];
+        }
     }
     if (gtid == 0) {
         q.q_start[S] = (int)all_tok;
         *q.num_cow = all_cows;
-        if (policy == PA_POOL_FIFO) p.hdr[3] = (int)(((long long)head + all_takes) % nb);
+        if (hdr.policy == PA_POOL_FIFO) p.hdr[3] = (int)(((long long)head + all_takes) % nb);
         p.hdr[4] = count - all_takes;
     }
 }
 
 // ----------------------------------------------------------------- release
 
-__global__ void __launch_bounds__(kThreads, 1) release_kernel(const ReleaseParams q) {
+template <int kPer> __global__ void __launch_bounds__(kThreads, 1) release_kernel(const ReleaseParams q) {
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -314,36 +385,45 @@ __global__ void __launch_bounds__(kThreads, 1) release_kernel(const ReleaseParam
     int *item_pre = dyn;             // [S + 1] 32-entry items before sequence s
     int *entries = item_pre + S + 1; // [S] entries sequence s drops
     __shared__ int sums[kWarps + 1];
-    __shared__ int s_bad[kCluster], s_freed[kCluster];  // of every CTA, written by each into all
+    __shared__ int s_bad[kClusterLarge], s_freed[kClusterLarge];  // of every CTA, written by each into all
 
     const Pool p = views(q.state, nb);
+    const Header hdr(p);
+    const int per = (S + kThreads - 1) / kThreads;
+    const int s0 = tid * per, s1 = min(S, s0 + per);
+    int n[kPer];          // entries that each sequence drops
+    unsigned gone = 0;    // bit i: sequence s0 + i is finished
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {  // in flight with the header
+        n[i] = 0;
+        if (s0 + i < s1) {
+            n[i] = __ldcg(q.ctx + s0 + i);
+            gone |= (unsigned)(__ldg(q.finished + s0 + i) != 0) << i;
+        }
+    }
     int bad = 0;  // PA_DEVERR_* bits
-    if (!header_ok(p, nb, bs)) {  // the same in every CTA, as in append_kernel
+    if (!hdr.ok(nb, bs)) {  // the same in every CTA, as in append_kernel
         if (rank == 0 && tid == 0) record_error(q.err, PA_DEVERR_POOL);
         return;
     }
-    const int head = __ldcg(p.hdr + 3), count = __ldcg(p.hdr + 4);
+    const int head = hdr.head, count = hdr.count;
 
     // ---- the items, in sequence order: 32 consecutive table entries of one
     // sequence each; a warp takes a run of consecutive items
-    const int per = (S + kThreads - 1) / kThreads;
-    const int s0 = tid * per, s1 = min(S, s0 + per);
-    int n[kPer], items = 0;
+    int items = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int s = s0 + i;
-        n[i] = 0;
-        if (s >= s1 || __ldg(q.finished + s) == 0) continue;
-        const int c = __ldcg(q.ctx + s);
-        if (c < 0 || c > (long long)MB * bs) {
+        if (!(gone >> i & 1u)) {
+            n[i] = 0;
+        } else if (n[i] < 0 || n[i] > (long long)MB * bs) {
             bad |= PA_DEVERR_CONTEXT;
-            continue;
+            n[i] = 0;
         }
-        n[i] = ceil_div(c, bs);
+        n[i] = ceil_div(n[i], bs);
         items += (n[i] + 31) / 32;
     }
     int all_items;
-    int at = block_exclusive<int>(items, sums, &all_items);
+    int at = block_exclusive(items, sums, &all_items);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int s = s0 + i;
@@ -356,47 +436,105 @@ __global__ void __launch_bounds__(kThreads, 1) release_kernel(const ReleaseParam
     __syncthreads();
     const int gwarp = rank * kWarps + warp, warps = ctas * kWarps;
     const int i0 = (int)((long long)all_items * gwarp / warps), i1 = (int)((long long)all_items * (gwarp + 1) / warps);
-    const int seq0 = i0 < i1 ? find_run(item_pre, S, i0) : 0;
-    // calls f(place, table entry pointer, block id) for this lane's entries, in order; f runs in all 32 lanes
-    // (pointer null where the lane has no entry)
-    auto each = [&](auto f) {
-        int s = seq0;
-        for (int it = i0; it < i1; ++it) {
-            while (item_pre[s + 1] <= it) ++s;
-            const int j = (it - item_pre[s]) * 32 + lane;
-            int32_t *e = j < entries[s] ? q.tables + (size_t)s * MB + j : nullptr;
-            const int id = e ? __ldcg(e) : -1;
-            f(it * 32 + lane, e, id);
+    // A warp's items go in batches whose memory accesses are all in flight at
+    // once; the entries of a single batch stay in registers, more than one are
+    // read again in each pass.
+    const bool single = i1 - i0 <= kBatch;
+    int entry[kBatch];         // this lane's table entry of each item of the batch (-1: none)
+    int id[kBatch];            // its block (-1: none)
+    int ref[kBatch];           // the block's count; for a shared block's last place, from the count of drops on, what is left of it
+    unsigned own = 0;          // bit k: the block is this sequence's alone (count 1)
+    unsigned last = 0;         // bit k: the last place that drops a shared block
+    auto load = [&](int b0) {
+        int s = b0 < i1 ? find_run(item_pre, S, b0) : 0;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int item = b0 + k;
+            entry[k] = -1;
+            if (item >= i1) continue;
+            while (item_pre[s + 1] <= item) ++s;
+            const int j = (item - item_pre[s]) * 32 + lane;
+            if (j < entries[s]) entry[k] = s * MB + j;
         }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) id[k] = entry[k] >= 0 ? __ldcg(q.tables + entry[k]) : -1;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (id[k] < 0 || id[k] >= nb) {
+                if (entry[k] >= 0) bad |= PA_DEVERR_BLOCK_ID;
+                id[k] = -1;
+            }
     };
+    auto place_of = [&](int b0, int k) { return (b0 + k) * 32 + lane; };
 
-    // ---- drops per block and the last place that drops it
-    each([&](int place, int32_t *e, int id) {
-        if (!e) return;
-        if (id < 0 || id >= nb) {
-            bad |= PA_DEVERR_BLOCK_ID;
-            return;
+    // ---- drops. A block of count 1 is claimed in one step: it is freed, here,
+    // unless the call is refused. A shared block counts its drops and the last
+    // place that drops it.
+    for (int b0 = i0; b0 < i1; b0 += kBatch) {
+        load(b0);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) ref[k] = id[k] >= 0 ? atomicCAS(p.ref + id[k], 1, kClaimed) : 0;
+        own = 0;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (id[k] < 0) continue;
+            if (ref[k] == 1) {
+                own |= 1u << k;
+            } else if (ref[k] > 1) {
+                atomicAdd(p.delta + id[k], 1);
+                atomicMax(p.last_old + id[k], place_of(b0, k));
+            } else {
+                bad |= PA_DEVERR_POOL;  // a free block, or one that is listed twice
+                id[k] = -1;
+            }
         }
-        if (__ldcg(p.ref + id) < 1) bad |= PA_DEVERR_POOL;
-        atomicAdd(p.delta + id, 1);
-        atomicMax(p.last_old + id, place);
-    });
+    }
     cluster.sync();
+
+    // The batch's entries again, where there are several batches; then bit k of
+    // the result: the entry frees its block.
+    auto look = [&](int b0) -> unsigned {
+        if (!single) {
+            load(b0);
+            own = 0;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) ref[k] = id[k] >= 0 ? __ldcg(p.ref + id[k]) : 0;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                if (id[k] >= 0 && ref[k] == kClaimed) own |= 1u << k;
+                else if (ref[k] < 1) id[k] = -1;
+            }
+        }
+        unsigned f = own;
+        last = 0;
+        int drops[kBatch], at_last[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const bool shared = id[k] >= 0 && !(own >> k & 1u);
+            drops[k] = shared ? __ldcg(p.delta + id[k]) : 0;
+            at_last[k] = shared ? __ldcg(p.last_old + id[k]) : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (at_last[k] == place_of(b0, k)) {
+                last |= 1u << k;
+                ref[k] -= drops[k];
+                if (ref[k] < 0) bad |= PA_DEVERR_POOL;
+                if (ref[k] == 0) f |= 1u << k;
+            }
+        return f;
+    };
 
     // ---- freed blocks, counted in place order
     int freed = 0;
-    auto valid = [&](int32_t *e, int id) { return e && id >= 0 && id < nb; };
-    each([&](int place, int32_t *e, int id) {
-        bool f = false;
-        if (valid(e, id)) {
-            const int d = __ldcg(p.delta + id), r = __ldcg(p.ref + id);
-            if (d > r) bad |= PA_DEVERR_POOL;
-            f = d == r && __ldcg(p.last_old + id) == place;
-        }
-        freed += __popc(__ballot_sync(0xffffffffu, f));
-    });
+    unsigned f = 0;
+    for (int b0 = i0; b0 < i1; b0 += kBatch) {
+        f = look(b0);
+        freed += __popc(f);
+    }
+    freed = __reduce_add_sync(0xffffffffu, freed);
     int cta_freed;
-    int base = block_exclusive<int>(lane == 0 ? freed : 0, sums, &cta_freed);
+    int base = block_exclusive(lane == 0 ? freed : 0, sums, &cta_freed);
     base = __shfl_sync(0xffffffffu, base, 0);
     if (bad) record_error(q.err, (unsigned)bad);
     bad = __syncthreads_or(bad);
@@ -417,45 +555,69 @@ __global__ void __launch_bounds__(kThreads, 1) release_kernel(const ReleaseParam
         bad = 1;
     }
 
-    // ---- apply: a block's last place lowers its count and, if it frees the block, hands it back
-    if (!bad) {
-        each([&](int place, int32_t *e, int id) {
-            bool f = false;
-            if (e && __ldcg(p.last_old + id) == place) {
-                const int d = __ldcg(p.delta + id), r = __ldcg(p.ref + id);
-                f = d == r;
-                p.ref[id] = r - d;
+    // ---- apply: freed blocks to the list's back, in place order; or claims taken back
+    const int back = head + count + base;  // below 2 nb, as is every place behind it
+    base = 0;
+    for (int b0 = i0; b0 < i1; b0 += kBatch) {
+        if (!single) f = look(b0);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const unsigned m = __ballot_sync(0xffffffffu, !bad && (f >> k & 1u));
+            if (m >> lane & 1u) {
+                const int to = back + base + __popc(m & ((1u << lane) - 1u));
+                p.ring[to < nb ? to : to - nb] = id[k];
             }
-            const unsigned m = __ballot_sync(0xffffffffu, f);
-            if (f) p.ring[((long long)head + count + base + __popc(m & ((1u << lane) - 1u))) % nb] = id;
             base += __popc(m);
-        });
+            if (own >> k & 1u) p.ref[id[k]] = bad ? 1 : 0;
+        }
     }
-    cluster.sync();  // every CTA is done with the marks and the lengths
+    cluster.sync();  // every CTA is done with the marks, shared counts, tables and lengths
 
-    each([&](int, int32_t *e, int id) {
-        if (!valid(e, id)) return;
-        p.delta[id] = 0;
-        p.last_old[id] = -1;
-        if (!bad) *e = -1;
-    });
+    // ---- shared counts, marks, table entries and lengths
+    for (int b0 = i0; b0 < i1; b0 += kBatch) {
+        if (!single) {
+            load(b0);
+            last = 0;
+            int at_last[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) at_last[k] = id[k] >= 0 ? __ldcg(p.last_old + id[k]) : -1;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (at_last[k] == place_of(b0, k)) {
+                    last |= 1u << k;
+                    ref[k] = __ldcg(p.ref + id[k]) - __ldcg(p.delta + id[k]);
+                }
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (last >> k & 1u) {
+                if (!bad) p.ref[id[k]] = ref[k];
+                p.delta[id[k]] = 0;
+                p.last_old[id[k]] = -1;
+            }
+            if (!bad && entry[k] >= 0) q.tables[entry[k]] = -1;
+        }
+    }
     if (!bad && tid / (kThreads / ctas) == rank) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-            if (s0 + i < s1 && __ldg(q.finished + s0 + i) != 0) q.ctx[s0 + i] = 0;
+            if (gone >> i & 1u) q.ctx[s0 + i] = 0;
     }
-    if (rank == 0 && tid == 0) {
-        if (!bad) p.hdr[4] = count + all_freed;
-    }
+    if (rank == 0 && tid == 0 && !bad) p.hdr[4] = count + all_freed;
 }
 
 // -------------------------------------------------------------------- host
 
+// What a kernel has been set up for, per device context.
+struct KernelCache {
+    AttrCache smem, large;
+};
+
+// Launches one cluster; `large`: of kClusterLarge CTAs, where the device can hold one.
 template <typename P>
-static cudaError_t launch_cluster(void (*kern)(P), const P &q, int smem, AttrCache *attr, int smem_max,
+static cudaError_t launch_cluster(void (*kern)(P), const P &q, int smem, KernelCache *cache, int smem_max, bool large,
                                   cudaStream_t stream) {
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), smem_max, attr);
-    if (e != cudaSuccess) return e;
+    const void *fn = reinterpret_cast<const void *>(kern);
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = kCluster;
@@ -468,6 +630,29 @@ static cudaError_t launch_cluster(void (*kern)(P), const P &q, int smem, AttrCac
     cfg.stream = stream;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    cudaError_t e = ensure_smem_attr(fn, smem_max, &cache->smem);
+    if (e != cudaSuccess) return e;
+    if (large) {
+        at[0].val.clusterDim.x = kClusterLarge;
+        cfg.gridDim = dim3(kClusterLarge);
+        int dev = 0;
+        e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev >= kCacheDevices) return cudaErrorInvalidDevice;
+        void *ctx = current_context();
+        if (ctx == nullptr || cache->large.ctx[dev].load(std::memory_order_acquire) != ctx) {
+            e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+            int fit = 0;
+            if (cudaOccupancyMaxActiveClusters(&fit, fn, &cfg) == cudaSuccess && fit > 0) {
+                cache->large.ctx[dev].store(current_context(), std::memory_order_release);
+            } else {
+                (void)cudaGetLastError();
+                at[0].val.clusterDim.x = kCluster;
+                cfg.gridDim = dim3(kCluster);
+            }
+        }
+    }
     return cudaLaunchKernelEx(&cfg, kern, q);
 }
 
@@ -518,9 +703,15 @@ extern "C" int pa_dpool_append(void *state, int num_blocks, int block_size, int3
     q.max_tokens = max_tokens;
     q.num_blocks = num_blocks;
     q.block_size = block_size;
-    static AttrCache attr;
-    constexpr int kMax = (3 * PA_DPOOL_MAX_SEQS + 2) * 4;
-    cudaError_t e = dpool::launch_cluster(dpool::append_kernel, q, (3 * num_seqs + 2) * 4, &attr, kMax, stream);
+    const int smem = (3 * num_seqs + 2) * 4;
+    const bool large = max_tokens > 65536;  // over two rounds of four slots for every thread of 8 CTAs
+    static dpool::KernelCache one, most;
+    cudaError_t e =
+        num_seqs <= dpool::kThreads
+            ? dpool::launch_cluster(dpool::append_kernel<1>, q, smem, &one, (3 * dpool::kThreads + 2) * 4, large,
+                                    stream)
+            : dpool::launch_cluster(dpool::append_kernel<dpool::kPerMost>, q, smem, &most,
+                                    (3 * PA_DPOOL_MAX_SEQS + 2) * 4, large, stream);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -544,8 +735,15 @@ extern "C" int pa_dpool_release(void *state, int num_blocks, int block_size, int
     q.max_blocks = max_blocks_per_seq;
     q.num_blocks = num_blocks;
     q.block_size = block_size;
-    static AttrCache attr;
-    constexpr int kMax = (2 * PA_DPOOL_MAX_SEQS + 1) * 4;
-    cudaError_t e = dpool::launch_cluster(dpool::release_kernel, q, (2 * num_seqs + 1) * 4, &attr, kMax, stream);
+    const int smem = (2 * num_seqs + 1) * 4;
+    // more table entries than the warps of 8 CTAs hold at once
+    const bool large = (long long)num_seqs * max_blocks_per_seq > 32ll * dpool::kBatch * dpool::kWarps * dpool::kCluster;
+    static dpool::KernelCache one, most;
+    cudaError_t e =
+        num_seqs <= dpool::kThreads
+            ? dpool::launch_cluster(dpool::release_kernel<1>, q, smem, &one, (2 * dpool::kThreads + 1) * 4, large,
+                                    stream)
+            : dpool::launch_cluster(dpool::release_kernel<dpool::kPerMost>, q, smem, &most,
+                                    (2 * PA_DPOOL_MAX_SEQS + 1) * 4, large, stream);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

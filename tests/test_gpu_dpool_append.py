@@ -236,3 +236,28 @@ def test_on_a_side_stream(pa):
     with torch.cuda.stream(st):
         b.append(np.arange(9), stream=st)
         b.release(np.arange(9) % 2)
+
+
+def test_release_of_many_entries(pa):
+    """More table entries than the warps hold at once (each pass reads them
+    again), shared and single blocks mixed; then the same refused."""
+    S, bs, MB = 40, 4, 3000
+    b = Both(pa, S, MB, 130000, bs, pa.PA_POOL_FIFO, 14, [(0, j, 9001) for j in (1, 2, 5)] + [(7, 8, 11990)])
+    rng = np.random.default_rng(15)
+    new = rng.integers(8000, 12001, S)
+    new = np.minimum(new, MB * bs - b.ctx)
+    b.append(new, pad=1)
+    for bad_at in ((30, 1500), (3, 7)):
+        keep = int(b.d_tables[bad_at])
+        for value, bit in ((130000, 0x1), (int(b.d_tables[0, 0]), 0x20), (int(b.d_tables[20, 5]), 0x20),
+                           (int(b.pool.free_list()[3]), 0x20)):
+            b.d_tables[bad_at] = value  # out of range; one drop too many of a shared block, of a single one; a free one
+            before = [t.clone() for t in (b.pool.state, b.d_tables, b.d_ctx)]
+            pa.pa_dpool_release(b.pool, b.d_tables, b.d_ctx, torch.ones(S, dtype=torch.int32, device="cuda"))
+            assert pa.pa_read_device_errors() == bit
+            for t, w in zip((b.pool.state, b.d_tables, b.d_ctx), before):
+                assert torch.equal(t, w)
+        b.d_tables[bad_at] = keep
+    b.release(rng.random(S) < 0.5)
+    b.release(np.ones(S, int))
+    assert b.host.num_free() == 130000
