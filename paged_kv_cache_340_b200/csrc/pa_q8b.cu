@@ -4,6 +4,7 @@
 //
 // Both move each byte once, so HBM bounds them.
 #include <cfloat>
+#include <type_traits>
 
 #include "pa_common.cuh"
 #include "pa_internal.h"
@@ -31,20 +32,39 @@ struct AppendParams {
 
 constexpr int kWarps = 8;
 
+template <typename T, int D, int BS> struct AppendShape {
+    static constexpr int kVec = 16 / sizeof(T);  // values of a lane's vector
+    static constexpr int kLanes = D / kVec;      // lanes of a row
+    static constexpr int kRows = 32 / kLanes;    // rows per warp load
+    static constexpr int kIt = BS / kRows;       // loads per full block
+    static constexpr bool kHold = kIt <= 16;     // 4 kIt registers hold the rows
+    static constexpr int kCtas = kIt <= 8 ? 4 : 3;
+};
+
 // Sequence s touches at most q_len / bs + 2 blocks, so numbering its blocks
 // from first_unit(q_start[s], s) on gives every block of every sequence a unit
 // of its own without a scan; a few units are empty.
 template <int BS> __device__ __forceinline__ int first_unit(int q0, int s) { return q0 / BS + 2 * s; }
 
-// The largest s with first_unit(q_start[s], s) <= u, searched 32 ways at a time by the warp.
+// The largest s with first_unit(q_start[s], s) <= u, searched by the warp 128
+// ways at a time, so that up to 128 sequences take one round of loads.
 template <int BS> __device__ __forceinline__ int unit_seq(const int32_t *q_start, int n, int u, int lane) {
+    constexpr int kWays = 4;  // probes a lane
     int lo = 0;
     while (n > 1) {
-        const int step = (n + 31) / 32;
-        const int k = lane * step;
-        const bool le = k < n && first_unit<BS>(__ldg(q_start + lo + k), lo + k) <= u;
-        const unsigned m = __ballot_sync(0xffffffffu, le);
-        const int last = m ? 31 - __clz(m) : 0;
+        const int step = (n + 32 * kWays - 1) / (32 * kWays);
+        bool le[kWays];
+#pragma unroll
+        for (int i = 0; i < kWays; ++i) {
+            const int k = (i * 32 + lane) * step;
+            le[i] = k < n && first_unit<BS>(__ldg(q_start + lo + min(k, n - 1)), lo + k) <= u;
+        }
+        int last = 0;
+#pragma unroll
+        for (int i = 0; i < kWays; ++i) {
+            const unsigned m = __ballot_sync(0xffffffffu, le[i]);
+            if (m) last = i * 32 + 31 - __clz(m);
+        }
         lo += last * step;
         n = min(step, n - last * step);
     }
@@ -56,27 +76,59 @@ __device__ __forceinline__ int code_of(float x, float inv) {
     return max(-127, min(127, __float2int_rn(__fmul_rn(x, inv))));
 }
 
-// One warp per (unit, head, K or V): the block's new rows, 16 bytes a lane.
+// Four codes of finite values none of which is above 127 / inv: the rounded
+// product plus 1.5 * 2^23 has the code in its low byte (the sum's rounding is
+// the rounding to a whole number, half to even), so nothing is converted or
+// clamped. (The product is rounded on its own: as two-wide mul.rn.f32x2 and
+// add.rn.f32x2 the pair came out fused, with other codes next to a half.)
+__device__ __forceinline__ uint32_t codes4(const float *x, float inv) {
+    uint32_t t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = __float_as_uint(__fadd_rn(__fmul_rn(x[i], inv), 12582912.f));
+    return __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+}
+
+// Magnitudes as unsigned numbers (the bits without the sign order like the
+// values, infinities and NaN above every finite one), 16-bit types two at a time.
+template <typename T> struct Magnitude {
+    static constexpr bool k32 = sizeof(T) == 4;
+    static constexpr uint32_t kInf = k32 ? 0x7f800000u : std::is_same_v<T, __half> ? 0x7c00u : 0x7f80u;
+    static __device__ __forceinline__ uint32_t larger(uint32_t m, uint32_t word) {
+        return k32 ? max(m, word & 0x7fffffffu) : __vmaxu2(m, word & 0x7fff7fffu);
+    }
+    // the warp's largest
+    static __device__ __forceinline__ uint32_t over_warp(uint32_t m) {
+        return __reduce_max_sync(0xffffffffu, k32 ? m : max(m & 0xffffu, m >> 16));
+    }
+    static __device__ __forceinline__ float value(uint32_t m) {
+        if constexpr (k32) return __uint_as_float(m);
+        else if constexpr (std::is_same_v<T, __half>) return __half2float(__ushort_as_half((unsigned short)m));
+        else return __uint_as_float(m << 16);
+    }
+};
+
+// One CTA per unit and part of the heads, one warp per (head, K or V) at a
+// time, 16 bytes a lane. The block's rows stay in registers between the search
+// for the largest value and the quantization (unless they take over 64 of
+// them), so HBM sees each byte once; about 4 instructions a value leave the
+// loads the bound (a first version with conversions, clamps and one (head, K or
+// V) per warp took 99 us where this one takes 67 for 2048-token prompts of 32
+// heads, 403 MB).
 template <typename T, int D, int BS>
-__global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendParams p) {
-    constexpr int kVec = 16 / sizeof(T);       // values of a lane's vector
-    constexpr int kLanes = D / kVec;           // lanes of a row
-    constexpr int kRows = 32 / kLanes;         // rows per warp load
-    constexpr int kIt = BS / kRows;            // loads per full block
-    // a block's rows stay in registers between the search for the largest
-    // value and the quantization, unless that would take over 64 of them
-    constexpr bool kHold = kIt <= 16;
+__global__ void __launch_bounds__(kWarps * 32, AppendShape<T, D, BS>::kCtas) append_kernel(const AppendParams p) {
+    using Sh = AppendShape<T, D, BS>;
+    using Mag = Magnitude<T>;
+    constexpr int kVec = Sh::kVec, kLanes = Sh::kLanes, kRows = Sh::kRows, kIt = Sh::kIt;
+    constexpr bool kHold = Sh::kHold;
     const int lane = threadIdx.x & 31;
-    const int which = blockIdx.y * kWarps + (threadIdx.x >> 5);
-    const int h = which >> 1, H = p.num_kv_heads;
-    const bool is_v = which & 1;
-    if (h >= H) return;
+    const int H = p.num_kv_heads;
     const int u = blockIdx.x;
     const int s = unit_seq<BS>(p.q_start, p.num_seqs, u, lane);
     const int q0 = __ldg(p.q_start + s), q1 = __ldg(p.q_start + s + 1);
     const int ctx = __ldg(p.ctx + s);
+    const bool first_warp = blockIdx.y == 0 && threadIdx.x < 32;
     if (q0 < 0 || q1 < q0 || q1 > p.num_tokens || q1 - q0 > ctx || ctx > (long long)p.max_blocks * BS) {
-        if (lane == 0 && which == 0) record_error(p.err, PA_DEVERR_CONTEXT);
+        if (first_warp && lane == 0) record_error(p.err, PA_DEVERR_CONTEXT);
         return;
     }
     const int p0 = ctx - (q1 - q0);                        // position of the first new token
@@ -85,72 +137,93 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendParams 
     if (a >= e) return;
     const int id = __ldg(p.tables + (size_t)s * p.max_blocks + lb);
     if (id < 0 || id >= p.num_blocks) {
-        if (lane == 0 && which == 0) record_error(p.err, PA_DEVERR_BLOCK_ID);
+        if (first_warp && lane == 0) record_error(p.err, PA_DEVERR_BLOCK_ID);
         return;
     }
     const int o0 = a - lb * BS, n = e - a;  // the new rows are slots o0 .. o0 + n - 1 of the block
     const int row = lane / kLanes, col = (lane % kLanes) * kVec;
-    const T *src = static_cast<const T *>(is_v ? p.value : p.key) + ((size_t)(q0 + a - p0) * H + h) * D + col;
-    float *scale = (is_v ? p.v_scale : p.k_scale) + (size_t)id * H + h;
-    int8_t *dst = (is_v ? p.v_cache : p.k_cache) + ((size_t)id * H + h) * (BS * D);
-    const float old = o0 > 0 ? *scale : 0.f;
+    for (int which = blockIdx.y * kWarps + (threadIdx.x >> 5); which < 2 * H; which += gridDim.y * kWarps) {
+        const int h = which >> 1;
+        const bool is_v = which & 1;
+        const T *src = static_cast<const T *>(is_v ? p.value : p.key) + ((size_t)(q0 + a - p0) * H + h) * D + col;
+        float *scale = (is_v ? p.v_scale : p.k_scale) + (size_t)id * H + h;
+        int8_t *dst = (is_v ? p.v_cache : p.k_cache) + ((size_t)id * H + h) * (BS * D);
+        const float old = o0 > 0 ? *scale : 0.f;
 
-    auto load = [&](int i) -> uint4 {
-        const int r = i * kRows + row;
-        return r < n ? __ldg(reinterpret_cast<const uint4 *>(src + (size_t)r * H * D)) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    uint4 held[kHold ? kIt : 1];
-    float amax = 0.f;
+        auto load = [&](int i) -> uint4 {
+            const int r = i * kRows + row;
+            return r < n ? __ldg(reinterpret_cast<const uint4 *>(src + (size_t)r * H * D)) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        uint4 held[kHold ? kIt : 1];
+        uint32_t mag = 0;
+        if constexpr (kHold) {
 #pragma unroll
-    for (int i = 0; i < kIt; ++i) {
-        const uint4 v = load(i);
-        if constexpr (kHold) held[i] = v;
-        float x[kVec];
-        Elt<T>::unpack(v, x);
-#pragma unroll
-        for (int c = 0; c < kVec; ++c) {
-            const float m = fabsf(x[c]);
-            amax = m <= FLT_MAX ? fmaxf(amax, m) : amax;  // finite values only
+            for (int i = 0; i < kIt; ++i) held[i] = load(i);
         }
-    }
 #pragma unroll
-    for (int mk = 16; mk >= 1; mk >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, mk));
-    float now = __fdiv_rn(amax, 127.f);
-    if (now < FLT_MIN) now = 0.f;
-    now = fmaxf(old, now);
-    const float inv = now > 0.f ? __fdiv_rn(1.f, now) : 0.f;
+        for (int i = 0; i < kIt; ++i) {
+            uint4 v;
+            if constexpr (kHold) v = held[i];
+            else v = load(i);
+            mag = Mag::larger(Mag::larger(mag, v.x), v.y);
+            mag = Mag::larger(Mag::larger(mag, v.z), v.w);
+        }
+        mag = Mag::over_warp(mag);
+        const bool finite = mag < Mag::kInf;  // the same in the whole warp
+        float amax = Mag::value(mag);
+        if (!finite) {  // rare: the largest finite value instead
+            amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < kIt; ++i) {
-        const int r = i * kRows + row;
-        if (r >= n) continue;
-        uint4 v;
-        if constexpr (kHold) v = held[i];
-        else v = load(i);
-        float x[kVec];
-        Elt<T>::unpack(v, x);
-        uint32_t w[kVec / 4];
+            for (int i = 0; i < kIt; ++i) {
+                float x[kVec];
+                if constexpr (kHold) Elt<T>::unpack(held[i], x);
+                else Elt<T>::unpack(load(i), x);
 #pragma unroll
-        for (int c = 0; c < kVec; c += 4)
-            w[c / 4] = (uint32_t)(code_of(x[c], inv) & 0xff) | (uint32_t)(code_of(x[c + 1], inv) & 0xff) << 8 |
-                       (uint32_t)(code_of(x[c + 2], inv) & 0xff) << 16 | (uint32_t)code_of(x[c + 3], inv) << 24;
-        int8_t *d = dst + (o0 + r) * D + col;
-        if constexpr (kVec == 8) *reinterpret_cast<uint2 *>(d) = make_uint2(w[0], w[1]);
-        else *reinterpret_cast<uint32_t *>(d) = w[0];
-    }
-    if (now > old) {
-        if (lane == 0) *scale = now;
-        if (o0 > 0) {  // the older rows' codes in the raised scale
-            const float ratio = __fdiv_rn(old, now);
-            for (int i = lane; i < o0 * D / 4; i += 32) {
-                uint32_t w = reinterpret_cast<uint32_t *>(dst)[i], r = 0;
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    r |= (uint32_t)(code_of((float)(int8_t)(w >> (8 * c)), ratio) & 0xff) << (8 * c);
-                reinterpret_cast<uint32_t *>(dst)[i] = r;
+                for (int c = 0; c < kVec; ++c) amax = fabsf(x[c]) <= FLT_MAX ? fmaxf(amax, fabsf(x[c])) : amax;
             }
+            amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
         }
-    } else if (o0 == 0 && lane == 0) {
-        *scale = now;  // a fresh block of zeros
+        float now = __fdiv_rn(amax, 127.f);
+        if (now < FLT_MIN) now = 0.f;
+        now = fmaxf(old, now);
+        const float inv = now > 0.f ? __fdiv_rn(1.f, now) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kIt; ++i) {
+            const int r = i * kRows + row;
+            if (r >= n) continue;
+            float x[kVec];
+            if constexpr (kHold) Elt<T>::unpack(held[i], x);
+            else Elt<T>::unpack(load(i), x);
+            uint32_t w[kVec / 4];
+#pragma unroll
+            for (int c = 0; c < kVec; c += 4) {
+                if (finite) {
+                    w[c / 4] = codes4(x + c, inv);
+                } else {
+                    w[c / 4] = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) w[c / 4] |= (uint32_t)(code_of(x[c + k], inv) & 0xff) << (8 * k);
+                }
+            }
+            int8_t *d = dst + (o0 + r) * D + col;
+            if constexpr (kVec == 8) *reinterpret_cast<uint2 *>(d) = make_uint2(w[0], w[1]);
+            else *reinterpret_cast<uint32_t *>(d) = w[0];
+        }
+        if (now > old) {
+            if (lane == 0) *scale = now;
+            if (o0 > 0) {  // the older rows' codes in the raised scale
+                const float ratio = __fdiv_rn(old, now);
+                for (int i = lane; i < o0 * D / 4; i += 32) {
+                    uint32_t w = reinterpret_cast<uint32_t *>(dst)[i], r = 0;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        r |= (uint32_t)(code_of((float)(int8_t)(w >> (8 * c)), ratio) & 0xff) << (8 * c);
+                    reinterpret_cast<uint32_t *>(dst)[i] = r;
+                }
+            }
+        } else if (o0 == 0 && lane == 0) {
+            *scale = now;  // a fresh block of zeros
+        }
     }
 }
 
@@ -173,8 +246,13 @@ __global__ void __launch_bounds__(256)
 
 template <typename T>
 static cudaError_t launch_append_t(const AppendParams &p, int head_dim, int block_size, cudaStream_t stream) {
-    const dim3 grid((unsigned)(p.num_tokens / block_size + 2 * p.num_seqs + 1),
-                    (unsigned)((2 * p.num_kv_heads + kWarps - 1) / kWarps));
+    const long long units = (long long)p.num_tokens / block_size + 2ll * p.num_seqs + 1;
+    // (head, K or V) pairs a warp takes one after another: up to 4, so that few
+    // warps pay for the lookups, as long as 8 CTAs an SM are left
+    const int warps_y = (2 * p.num_kv_heads + kWarps - 1) / kWarps;
+    long long per = units * warps_y / (8ll * sm_count());
+    per = per < 1 ? 1 : per > 4 ? 4 : per;
+    const dim3 grid((unsigned)units, (unsigned)((warps_y + per - 1) / per));
     if (head_dim == 128) {
         if (block_size == 16) append_kernel<T, 128, 16><<<grid, kWarps * 32, 0, stream>>>(p);
         else append_kernel<T, 128, 32><<<grid, kWarps * 32, 0, stream>>>(p);
