@@ -21,8 +21,8 @@
 //
 // A work item is a (sequence, kv head, up to 8 of its query heads[,
 // partition]); the grid has one block per item. A resident CTA takes over
-// blocks that have not started yet (clusterlaunchcontrol.try_cancel), one ahead
-// of the item it works on, so K and V tiles of the next item stream in while the
+// blocks that have not started yet (clusterlaunchcontrol.try_cancel), some tiles
+// ahead of its work, so K and V tiles of the next item stream in while the
 // last one ends: a CTA per item lost about 3 us to each item's first lookups.
 // A tile is 128 rows of 128 bytes of K and of V. A row is one token at
 // head_dim 128 and two neighbouring tokens at 64: there each query head has two
@@ -30,7 +30,7 @@
 // query padded with zeros over the other half, and the two are joined at the
 // end.
 //   * warp 7 claims the items, looks up what the other warps need of them and
-//     writes the query's digits, two items deep;
+//     writes the query's digits, a few items deep;
 //   * warps 5 and 6 load the K and the V tiles, one lane a block, through the
 //     table with 2-D TMA copies in the 128-byte swizzled layout, two stages
 //     each; warp 5 also puts the tile's block scales beside them;
@@ -88,9 +88,8 @@ constexpr int kG = 8;                          // query heads per item, at most
 constexpr int kRowBytes = 128;
 constexpr int kTile = 128 * kRowBytes;         // 16 KB of K or V
 constexpr int kStages = 2;
-constexpr int kItems = 2;                      // items known ahead, the current one included
 constexpr int kScales = 4;                     // tiles whose scales are kept: warp 5 is at most three tiles ahead
-constexpr int kClaimAhead = 4;                 // tiles of an item still to be loaded when the next one is claimed
+constexpr int kClaimAhead = 4;                 // tiles still to be loaded when another item is claimed
 constexpr int kMaxBlocks = 16;                 // blocks of a tile, at most
 constexpr int kSoftmaxThreads = 128;
 constexpr int kMmaWarp = 4, kLoadK = 5, kLoadV = 6, kItemWarp = 7;
@@ -123,6 +122,7 @@ struct Scales {
 // reads, so those rows are whatever lies behind.
 template <int V> struct Shape {
     static constexpr int kN = (3 * V + 15) / 16 * 16;          // MMA columns
+    static constexpr int kItems = V <= 2 ? 4 : V <= 4 ? 3 : 2;  // items known at a time (as shared memory allows)
     static constexpr int kDigits = (3 * V + 7) / 8 * 1024;     // bytes of 3 V digit rows, in 8-row groups
     static constexpr int kOffK = 0;
     static constexpr int kOffV = kOffK + kStages * kTile;
@@ -134,7 +134,7 @@ template <int V> struct Shape {
     static constexpr int kOffMax = kOffQs + kItems * V * 4;    // float [2][4 warps][V], tiles in turn
     static constexpr int kOffClc = (kOffMax + 8 * V * 4 + 15) / 16 * 16;
     static constexpr int kOffBar = kOffClc + 16;
-    static constexpr int kBars = 4 * kStages + 2 + 4 + 2 * kItems + 1;
+    static constexpr int kBars = 4 * kStages + 2 + 3 + 2 * kItems + 1;
     static constexpr int kEnd = kOffBar + kBars * 8 + 16;
     static constexpr int kReadEnd = kOffP + kN * kRowBytes;    // the last byte a product may read
     static constexpr int kSmemBytes = kEnd > kReadEnd ? kEnd : kReadEnd;
@@ -281,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
     constexpr int kCols3 = (3 * kV + 3) / 4 * 4;  // S columns read: three a virtual head
     constexpr int kOCols3 = (3 * G + 3) / 4 * 4;  // O columns read: those of the lane's own tokens
     constexpr int kTok = 128 * kPar;              // tokens per tile
+    constexpr int kItems = Sh::kItems;
 
     extern __shared__ __align__(1024) unsigned char sm[];
     unsigned char *Ps = sm + Sh::kOffP;
@@ -296,10 +297,10 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
     uint64_t *o_full = s_full + 3;           // O of the tile computed
     uint64_t *idle = s_full + 4;             // every product issued has finished
     uint64_t *clc = s_full + 5;              // the answer to a claim
-    uint64_t *claim = s_full + 6;            // warp 5 nears the end of an item: claim the next
-    uint64_t *i_full = s_full + 7, *i_empty = i_full + kItems;  // an item is described; everybody is done with it
+    uint64_t *i_full = s_full + 6, *i_empty = i_full + kItems;  // an item is described; everybody is done with it
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Sh::kBars);
     volatile int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
+    volatile int *loaded = reinterpret_cast<int *>(tmem_slot + 2);  // tiles that warp 5 has asked for
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int bs_shift = p.bs_shift;
@@ -327,12 +328,12 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
         mbar_init(o_full, 1);
         mbar_init(idle, 1);
         mbar_init(clc, 1);
-        mbar_init(claim, 1);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(i_full + i, 1);
             mbar_init(i_empty + i, 7);  // warps 0-6
         }
         *abort_flag = 0;
+        *loaded = 0;
         fence_mbar_init();
         fence_proxy_async_smem();
     }
@@ -353,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
             // ======================================================= item warp
             int x = blockIdx.x, y = blockIdx.y, z = blockIdx.z;
             bool more = true, sound = true;
+            int tiles = 0;  // of all items so far
             for (int n = 0; sound; ++n) {
                 const int slot = n % kItems;
                 if (n >= kItems) {
@@ -466,10 +468,18 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(i_full + slot);
-                // ---- the next one, once warp 5 is near the end of this one
+                // ---- the next one, once few tiles are left to load
+                tiles += ntiles;
                 more = false;
                 if (p.steal) {
-                    sound = __all_sync(0xffffffffu, mbar_wait(claim, n & 1) && !*abort_flag);
+                    if (tiles - *loaded > kClaimAhead) {
+                        const uint64_t t0 = global_ns();
+                        for (uint32_t i = 1; sound && tiles - *loaded > kClaimAhead; ++i) {
+                            __nanosleep(64);
+                            if (*abort_flag || ((i & 63u) == 0u && global_ns() - t0 > kWaitLimitNs * 4)) sound = false;
+                        }
+                    }
+                    sound = __all_sync(0xffffffffu, sound && !*abort_flag);
                     if (!sound) break;
                     if (lane == 0) {
                         fence_proxy_async_smem();  // the last answer has been read
@@ -504,10 +514,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
                 const int32_t *trow = p.tables + (size_t)it.s * p.max_blocks;
                 int id = lane < kMaxBlocks ? it.ids[lane] : -1;
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(i_empty + slot);
-                    if (!is_v && p.steal && ntiles < kClaimAhead) mbar_arrive(claim);
-                }
+                if (lane == 0) mbar_arrive(i_empty + slot);
                 auto look = [&](int j) -> int {
                     const int lb = b0 + j * blocks + lane;
                     return (lane < blocks && lb < nblk) ? __ldg(trow + lb) : -1;
@@ -543,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
                         __syncwarp();
                         if (lane == 0) {
                             mbar_arrive(full + b);
-                            if (p.steal && ntiles >= kClaimAhead && j == ntiles - kClaimAhead) mbar_arrive(claim);
+                            *loaded = t + 1;
                         }
                     }
                     id = id_next;
