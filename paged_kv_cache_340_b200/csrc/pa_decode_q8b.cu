@@ -90,6 +90,9 @@ constexpr int kTile = 128 * kRowBytes;         // 16 KB of K or V
 constexpr int kStages = 2;
 constexpr int kScales = 4;                     // tiles whose scales are kept: warp 5 is at most three tiles ahead
 constexpr int kClaimAhead = 4;                 // tiles still to be loaded when another item is claimed
+// Splitting along the tokens, in tiles: 16-tile pieces measured best of 8, 12,
+// 16, 32 and 64 for 8 sequences of 32,768 to 131,072 tokens (163, 161, 158, 172, 195 us).
+constexpr int kPiece = 16, kPieceMost = 48;
 constexpr int kMaxBlocks = 16;                 // blocks of a tile, at most
 constexpr int kSoftmaxThreads = 128;
 constexpr int kMmaWarp = 4, kLoadK = 5, kLoadV = 6, kItemWarp = 7;
@@ -131,10 +134,10 @@ template <int V> struct Shape {
     static constexpr int kOffScales = kOffP + kDigits;
     static constexpr int kOffItems = kOffScales + kScales * (int)sizeof(Scales);
     static constexpr int kOffQs = kOffItems + kItems * (int)sizeof(Item);  // float [kItems][V]: log2 score per digit unit
-    static constexpr int kOffMax = kOffQs + kItems * V * 4;    // float [2][4 warps][V], tiles in turn
+    static constexpr int kOffMax = (kOffQs + kItems * V * 4 + 15) / 16 * 16;  // float [2][4 warps][V], tiles in turn
     static constexpr int kOffClc = (kOffMax + 8 * V * 4 + 15) / 16 * 16;
     static constexpr int kOffBar = kOffClc + 16;
-    static constexpr int kBars = 4 * kStages + 2 + 3 + 2 * kItems + 1;
+    static constexpr int kBars = 4 * kStages + 2 + 3 + 3 * kItems + 1;
     static constexpr int kEnd = kOffBar + kBars * 8 + 16;
     static constexpr int kReadEnd = kOffP + kN * kRowBytes;    // the last byte a product may read
     static constexpr int kSmemBytes = kEnd > kReadEnd ? kEnd : kReadEnd;
@@ -228,6 +231,26 @@ __device__ __forceinline__ bool softmax_sync_and(bool v) {
     return all != 0;
 }
 
+// Sums of N values per lane over the warp. While a lane has several, it keeps
+// half of them and gives the others away, so lane i ends with the sum of value
+// i * N / 32 in x[0].
+template <int N, int Mask> __device__ __forceinline__ void warp_sums(float *x, int lane) {
+    if constexpr (Mask >= 1) {
+        if constexpr (N > 1) {
+            const bool upper = (lane & Mask) != 0;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                const float give = upper ? x[i] : x[i + N / 2], keep = upper ? x[i + N / 2] : x[i];
+                x[i] = keep + __shfl_xor_sync(0xffffffffu, give, Mask);
+            }
+            warp_sums<N / 2, Mask / 2>(x, lane);
+        } else {
+            x[0] += __shfl_xor_sync(0xffffffffu, x[0], Mask);
+            warp_sums<1, Mask / 2>(x, lane);
+        }
+    }
+}
+
 __device__ __forceinline__ float warp_max(float x) {
     float y;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
@@ -297,7 +320,9 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
     uint64_t *o_full = s_full + 3;           // O of the tile computed
     uint64_t *idle = s_full + 4;             // every product issued has finished
     uint64_t *clc = s_full + 5;              // the answer to a claim
-    uint64_t *i_full = s_full + 6, *i_empty = i_full + kItems;  // an item is described; everybody is done with it
+    uint64_t *i_full = s_full + 6;           // [kItems] an item is described
+    uint64_t *q_full = i_full + kItems;      // [kItems] and its query's digits are there
+    uint64_t *i_empty = q_full + kItems;     // [kItems] everybody is done with it
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Sh::kBars);
     volatile int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
     volatile int *loaded = reinterpret_cast<int *>(tmem_slot + 2);  // tiles that warp 5 has asked for
@@ -330,6 +355,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
         mbar_init(clc, 1);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(i_full + i, 1);
+            mbar_init(q_full + i, 1);
             mbar_init(i_empty + i, 7);  // warps 0-6
         }
         *abort_flag = 0;
@@ -363,9 +389,11 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
                 }
                 Item &it = items[slot];
                 if (!more) {
+                    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up
                     if (lane == 0) {
                         it.ntiles = -1;
                         mbar_arrive(i_full + slot);
+                        mbar_arrive(q_full + slot);
                     }
                     break;
                 }
@@ -419,23 +447,25 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
                     it.part = x;
                     it.write = write;
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(i_full + slot);  // the load warps can start
                 // ---- the query's digits
                 unsigned char *Qs = sm + Sh::kOffQ + slot * Sh::kDigits;
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     const T *raw_g = reinterpret_cast<const T *>(&raw[g]);
-                    float q[kE], amax = 0.f, odd = 0.f;  // odd: NaN if an element is not finite
+                    float q[kE];
+                    uint32_t mag = 0;  // the largest |q|, as bits (they order like the values, infinities and NaN on top)
 #pragma unroll
                     for (int e = 0; e < kE; ++e) {
                         q[e] = (float)raw_g[e];
-                        amax = fmaxf(amax, fabsf(q[e]));
-                        odd += q[e] * 0.f;
+                        mag = max(mag, __float_as_uint(q[e]) & 0x7fffffffu);
                     }
-                    amax = warp_max(amax);
-#pragma unroll
-                    for (int mk = 16; mk >= 1; mk >>= 1) odd += __shfl_xor_sync(0xffffffffu, odd, mk);
+                    mag = __reduce_max_sync(0xffffffffu, mag);
+                    const float amax = __uint_as_float(mag);
+                    const bool finite = mag < 0x7f800000u;
                     // a query below 2^-100 counts as zero (its unit's reciprocal would not be finite)
-                    const bool live = amax >= 7.888609e-31f && odd == 0.f;
+                    const bool live = finite && amax >= 7.888609e-31f;
                     const float inv = live ? kQUnit / amax : 0.f;
                     uint32_t w[3] = {0u, 0u, 0u};  // the lane's kE digits of each place
 #pragma unroll
@@ -463,11 +493,13 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
                                 *reinterpret_cast<uint16_t *>(at(1 - par)) = 0;
                             }
                         }
-                    if (lane < kPar) qscale[slot * kV + lane * G + g] = (live ? amax / kQUnit : 0.f) * p.scale_log2 + odd;
+                    // (a query that is not finite makes its scores, and so its row, NaN)
+                    if (lane < kPar)
+                        qscale[slot * kV + lane * G + g] = live ? amax / kQUnit * p.scale_log2 : finite ? 0.f : NAN;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(i_full + slot);
+                if (lane == 0) mbar_arrive(q_full + slot);
                 // ---- the next one, once few tiles are left to load
                 tiles += ntiles;
                 more = false;
@@ -576,8 +608,8 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
                         // The next item. It may be described only after an item has
                         // ended whose O is still to be issued here, so that goes first.
                         const int next = (n + 1) % kItems;
-                        if (done == issued || mbar_test(i_full + next, ((n + 1) / kItems) & 1)) {
-                            sound = mbar_wait(i_full + next, ((n + 1) / kItems) & 1) && !*abort_flag;
+                        if (done == issued || mbar_test(q_full + next, ((n + 1) / kItems) & 1)) {
+                            sound = mbar_wait(q_full + next, ((n + 1) / kItems) & 1) && !*abort_flag;
                             if (!sound) break;
                             if (n >= 0) mbar_arrive(i_empty + slot);
                             ++n;
@@ -641,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
         bool ok = true;
         for (int n = 0; ok; ++n) {
             const int slot = n % kItems;
-            bool sound = __all_sync(0xffffffffu, mbar_wait(i_full + slot, (n / kItems) & 1) && !*abort_flag);
+            bool sound = __all_sync(0xffffffffu, mbar_wait(q_full + slot, (n / kItems) & 1) && !*abort_flag);
             ok = softmax_sync_and(sound);
             if (!ok) break;
             const Item &it = items[slot];
@@ -716,9 +748,22 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
                 ok = softmax_sync_and(sound);
                 if (!ok) break;
                 float mt[kV];
+                if constexpr (kV % 4 == 0) {
 #pragma unroll
-                for (int v = 0; v < kV; ++v)
-                    mt[v] = fmaxf(fmaxf(wm[v], wm[kV + v]), fmaxf(wm[2 * kV + v], wm[3 * kV + v]));
+                    for (int v = 0; v < kV; v += 4) {
+                        float4 w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4 *>(wm + i * kV + v);
+                        mt[v] = fmaxf(fmaxf(w[0].x, w[1].x), fmaxf(w[2].x, w[3].x));
+                        mt[v + 1] = fmaxf(fmaxf(w[0].y, w[1].y), fmaxf(w[2].y, w[3].y));
+                        mt[v + 2] = fmaxf(fmaxf(w[0].z, w[1].z), fmaxf(w[2].z, w[3].z));
+                        mt[v + 3] = fmaxf(fmaxf(w[0].w, w[1].w), fmaxf(w[2].w, w[3].w));
+                    }
+                } else {
+#pragma unroll
+                    for (int v = 0; v < kV; ++v)
+                        mt[v] = fmaxf(fmaxf(wm[v], wm[kV + v]), fmaxf(wm[2 * kV + v], wm[3 * kV + v]));
+                }
                 if (j > 0) {  // O of the tile before is there: P and O are free once it is added up
                     sound = __all_sync(0xffffffffu, mbar_wait(o_full, (t - 1) & 1) && !*abort_flag);
                     if (!sound) continue;  // (the next barrier tells the others)
@@ -757,14 +802,11 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
 #pragma unroll
             for (int v = 0; v < kV; ++v) {
                 const float mw = warp_max(m_l[v]);
-                float lw = m_l[v] > -INFINITY ? l[v] * fast_exp2(m_l[v] - mw) : l[v];
-#pragma unroll
-                for (int mk = 16; mk >= 1; mk >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, mk);
-                if (lane == 0) {
-                    red_m[warp * kV + v] = mw;
-                    red_l[warp * kV + v] = lw;
-                }
+                if (m_l[v] > -INFINITY) l[v] *= fast_exp2(m_l[v] - mw);
+                if (lane == 0) red_m[warp * kV + v] = mw;
             }
+            warp_sums<kV, 16>(l, lane);  // lane c * 32 / kV holds head c's
+            if (lane % (32 / kV) == 0) red_l[warp * kV + lane / (32 / kV)] = l[0];
             named_bar_sync(1, kSoftmaxThreads);
             float m[G], sum[G];
 #pragma unroll
@@ -814,11 +856,15 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
 }
 
 // Joins the partitions: out = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) l_p.
-// One CTA per (head, sequence); warp w takes partitions w, w + 4, .., a lane
-// D / 32 dims, and the warps are joined in shared memory.
-template <int D> __global__ void __launch_bounds__(128) join_kernel(const DecodeParams p) {
+// One CTA per (head, sequence); warp w takes partitions w, w + kJoinWarps, ..,
+// a lane D / 32 dims, and the warps are joined in shared memory. A batch of
+// kJoinWarps * kU partitions costs one trip to L2, which is all that bounds it.
+constexpr int kJoinWarps = 16;
+
+template <int D> __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const DecodeParams p) {
     constexpr int kE = D / 32, kU = 4;
-    __shared__ float sm_m[4], sm_l[4], sm_o[4][D];
+    using Vec = std::conditional_t<kE == 4, float4, float2>;
+    __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps], sm_o[kJoinWarps][D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int s = blockIdx.y;
     if (p.seq_order) {
@@ -830,17 +876,17 @@ template <int D> __global__ void __launch_bounds__(128) join_kernel(const Decode
     const int n = (L + p.partition_size - 1) / p.partition_size;
     const size_t row = (size_t)s * p.num_heads + blockIdx.x;
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml) + row * p.max_parts;
-    const float *acc = p.ws_acc + row * p.max_parts * D + lane * kE;
+    const Vec *acc = reinterpret_cast<const Vec *>(p.ws_acc + row * p.max_parts * D) + lane;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // decode_kernel's partitions are written
     float m = -INFINITY, l = 0.f, o[kE] = {};
-    for (int i0 = warp; i0 < n; i0 += 4 * kU) {
+    for (int i0 = warp; i0 < n; i0 += kJoinWarps * kU) {
         float2 v[kU];
-        float a[kU][kE];
+        Vec a[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {  // kU partitions' loads in flight
-            const int i = i0 + 4 * u;
-            v[u] = i < n ? ml[i] : make_float2(-INFINITY, 0.f);
-#pragma unroll
-            for (int e = 0; e < kE; ++e) a[u][e] = i < n ? acc[(size_t)i * D + e] : 0.f;
+            const int i = i0 + kJoinWarps * u;
+            v[u] = i < n ? __ldcg(ml + i) : make_float2(-INFINITY, 0.f);
+            a[u] = i < n ? __ldcg(acc + (size_t)i * 32) : Vec{};
         }
         float mn = m;
 #pragma unroll
@@ -855,7 +901,7 @@ template <int D> __global__ void __launch_bounds__(128) join_kernel(const Decode
             const float w = v[u].x > -INFINITY ? fast_exp2(v[u].x - m) : 0.f;
             l += v[u].x > -INFINITY ? w * v[u].y : v[u].y;  // (a NaN sum stays)
 #pragma unroll
-            for (int e = 0; e < kE; ++e) o[e] = fmaf(w, a[u][e], o[e]);
+            for (int e = 0; e < kE; ++e) o[e] = fmaf(w, reinterpret_cast<const float *>(&a[u])[e], o[e]);
         }
     }
     if (lane == 0) {
@@ -867,10 +913,12 @@ template <int D> __global__ void __launch_bounds__(128) join_kernel(const Decode
     __syncthreads();
     const int d = threadIdx.x;
     if (d >= D) return;
-    const float M = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, sm_m[w]);
     float num = 0.f, den = 0.f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < kJoinWarps; ++w) {
         const float f = sm_m[w] > -INFINITY ? fast_exp2(sm_m[w] - M) : 0.f;
         num = fmaf(f, sm_o[w][d], num);
         den += sm_m[w] > -INFINITY ? f * sm_l[w] : sm_l[w];
@@ -912,16 +960,17 @@ static cudaError_t launch_decode(const CUtensorMap &km, const CUtensorMap &vm, c
 #undef PA_Q8B
 }
 
-// Tokens of a partition: 0 where the (sequence, kv head) pairs alone give the
-// GPU enough CTAs, or a sequence is one tile.
-static int partition_of(int num_seqs, int rows_y, int head_dim, int max_ctx) {
+// Tokens of a partition (0: none). One item per resident CTA, as far as the
+// longest context tells, where that leaves a CTA at most kPieceMost tiles; longer
+// work goes in pieces of about kPiece tiles, which the CTAs take one after
+// another, so that ragged lengths even out.
+static int partition_of(int num_seqs, int rows_y, int group, int head_dim, int max_ctx) {
     const int tok = 128 * (128 / head_dim);
     const long long items = (long long)num_seqs * rows_y, tiles = ((long long)max_ctx + tok - 1) / tok;
-    const long long target = 6ll * sm_count();
-    if (items >= target / 2 || tiles < 2) return 0;
-    long long parts = (target + items - 1) / items;
-    if (parts > tiles) parts = tiles;
-    const long long per = (tiles + parts - 1) / parts;
+    const long long ctas = (group > 4 && head_dim == 64 ? 2ll : 3ll) * sm_count();
+    if (items >= ctas || tiles < 2) return 0;
+    long long per = (items * tiles + ctas - 1) / ctas;
+    if (per > kPieceMost) per = kPiece;
     return per >= tiles ? 0 : (int)(per * tok);
 }
 
@@ -944,7 +993,7 @@ extern "C" size_t pa_decode_q8b_workspace_bytes(int num_seqs, int num_heads, int
         q8b::rows_of(num_heads, num_kv_heads) > 65535)
         return 0;
     const int rows_y = (int)q8b::rows_of(num_heads, num_kv_heads);
-    const int P = q8b::partition_of(num_seqs, rows_y, head_dim, max_context_len);
+    const int P = q8b::partition_of(num_seqs, rows_y, num_heads / num_kv_heads, head_dim, max_context_len);
     // at least 16 bytes, so that a workspace of the size asked for is always one
     return P ? pa_splitk_workspace_bytes(num_seqs, num_heads, head_dim, max_context_len, P) : 16;
 }
@@ -1000,7 +1049,7 @@ extern "C" int pa_decode_q8b(void *out, const void *query, pa_dtype q_dtype, con
     p.scale_log2 = scale * 1.4426950408889634f;
     p.out_dtype = out_dtype;
     p.max_parts = 1;
-    const int P = workspace ? q8b::partition_of(num_seqs, (int)rows_y, head_dim, max_context_len) : 0;
+    const int P = workspace ? q8b::partition_of(num_seqs, (int)rows_y, group, head_dim, max_context_len) : 0;
     if (P) {
         p.partition_size = P;
         p.max_parts = (max_context_len + P - 1) / P;
@@ -1020,10 +1069,18 @@ extern "C" int pa_decode_q8b(void *out, const void *query, pa_dtype q_dtype, con
     cudaError_t e = q_dtype == PA_F16 ? q8b::launch_decode<__half>(km, vm, p, head_dim, stream)
                                       : q8b::launch_decode<__nv_bfloat16>(km, vm, p, head_dim, stream);
     if (e == cudaSuccess && P) {
-        const dim3 grid((unsigned)num_heads, (unsigned)num_seqs);
-        if (head_dim == 128) q8b::join_kernel<128><<<grid, 128, 0, stream>>>(p);
-        else q8b::join_kernel<64><<<grid, 128, 0, stream>>>(p);
-        e = cudaGetLastError();
+        // launched while the last items run (programmatic dependent launch)
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)num_heads, (unsigned)num_seqs);
+        cfg.blockDim = dim3(q8b::kJoinWarps * 32);
+        cfg.stream = stream;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        e = head_dim == 128 ? cudaLaunchKernelEx(&cfg, q8b::join_kernel<128>, p)
+                            : cudaLaunchKernelEx(&cfg, q8b::join_kernel<64>, p);
     }
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
