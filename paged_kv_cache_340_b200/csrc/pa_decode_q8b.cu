@@ -51,6 +51,7 @@
 
 #include "pa_common.cuh"
 #include "pa_internal.h"
+#include "pa_pdl.cuh"
 
 namespace pa {
 namespace q8b {
@@ -337,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
     };
 
     if (smem_addr(sm) & 1023u) {  // the swizzled layouts count on it
+        wait_previous();
         if (tid == 0) record_error(p.err, PA_DEVERR_TIMEOUT);
         return;
     }
@@ -372,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
     fence_before();
     __syncthreads();
     fence_after();
+    wait_previous();
     const uint32_t tmem = *tmem_slot;
 
     if (warp >= 4) {
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
                 }
                 Item &it = items[slot];
                 if (!more) {
-                    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up
+                    allow_next();
                     if (lane == 0) {
                         it.ntiles = -1;
                         mbar_arrive(i_full + slot);
@@ -865,6 +868,8 @@ template <int D> __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(
     constexpr int kE = D / 32, kU = 4;
     using Vec = std::conditional_t<kE == 4, float4, float2>;
     __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps], sm_o[kJoinWarps][D];
+    wait_previous();  // decode_kernel's partitions are written
+    allow_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int s = blockIdx.y;
     if (p.seq_order) {
@@ -877,7 +882,6 @@ template <int D> __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(
     const size_t row = (size_t)s * p.num_heads + blockIdx.x;
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml) + row * p.max_parts;
     const Vec *acc = reinterpret_cast<const Vec *>(p.ws_acc + row * p.max_parts * D) + lane;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // decode_kernel's partitions are written
     float m = -INFINITY, l = 0.f, o[kE] = {};
     for (int i0 = warp; i0 < n; i0 += kJoinWarps * kU) {
         float2 v[kU];
@@ -945,8 +949,7 @@ static cudaError_t launch_decode_t(const CUtensorMap &km, const CUtensorMap &vm,
     const dim3 grid(p.max_parts, p.num_kv_heads * p.sub_groups, p.num_seqs);
     // blocks that all start at once leave none to take over
     p.steal = (long long)grid.x * grid.y * grid.z > (long long)Sh::kCtas * sm_count();
-    kern<<<grid, kThreads, Sh::kSmemBytes, stream>>>(km, vm, p);
-    return cudaGetLastError();
+    return launch_after(kern, grid, kThreads, Sh::kSmemBytes, 1, stream, km, vm, p);
 }
 
 template <typename T>
@@ -1069,18 +1072,10 @@ extern "C" int pa_decode_q8b(void *out, const void *query, pa_dtype q_dtype, con
     cudaError_t e = q_dtype == PA_F16 ? q8b::launch_decode<__half>(km, vm, p, head_dim, stream)
                                       : q8b::launch_decode<__nv_bfloat16>(km, vm, p, head_dim, stream);
     if (e == cudaSuccess && P) {
-        // launched while the last items run (programmatic dependent launch)
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[0].val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)num_heads, (unsigned)num_seqs);
-        cfg.blockDim = dim3(q8b::kJoinWarps * 32);
-        cfg.stream = stream;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        e = head_dim == 128 ? cudaLaunchKernelEx(&cfg, q8b::join_kernel<128>, p)
-                            : cudaLaunchKernelEx(&cfg, q8b::join_kernel<64>, p);
+        const dim3 grid((unsigned)num_heads, (unsigned)num_seqs);
+        const unsigned block = q8b::kJoinWarps * 32;
+        e = head_dim == 128 ? launch_after(q8b::join_kernel<128>, grid, block, 0, 1, stream, p)
+                            : launch_after(q8b::join_kernel<64>, grid, block, 0, 1, stream, p);
     }
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -28,6 +28,7 @@
 #include "pa_common.cuh"
 #include "pa_dpool.cuh"
 #include "pa_internal.h"
+#include "pa_pdl.cuh"
 
 namespace pa {
 namespace dpool {
@@ -172,6 +173,8 @@ template <int kPer> __global__ void __launch_bounds__(kThreads, 1) append_kernel
     int *ctx_cow = take_pre + S + 1;     // [S] context length, sign bit: its last block is copied
     __shared__ long long sums[2 * (kWarps + 1)];
 
+    wait_previous();
+    allow_next();
     const Pool p = views(q.state, nb);
     const Header hdr(p);
     const int per = (S + kThreads - 1) / kThreads;
@@ -387,6 +390,8 @@ template <int kPer> __global__ void __launch_bounds__(kThreads, 1) release_kerne
     __shared__ int sums[kWarps + 1];
     __shared__ int s_bad[kClusterLarge], s_freed[kClusterLarge];  // of every CTA, written by each into all
 
+    wait_previous();
+    allow_next();
     const Pool p = views(q.state, nb);
     const Header hdr(p);
     const int per = (S + kThreads - 1) / kThreads;
@@ -618,42 +623,38 @@ template <typename P>
 static cudaError_t launch_cluster(void (*kern)(P), const P &q, int smem, KernelCache *cache, int smem_max, bool large,
                                   cudaStream_t stream) {
     const void *fn = reinterpret_cast<const void *>(kern);
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = kCluster;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kCluster);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = stream;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
     cudaError_t e = ensure_smem_attr(fn, smem_max, &cache->smem);
     if (e != cudaSuccess) return e;
+    unsigned ctas = kCluster;
     if (large) {
-        at[0].val.clusterDim.x = kClusterLarge;
-        cfg.gridDim = dim3(kClusterLarge);
         int dev = 0;
         e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
         if (dev >= kCacheDevices) return cudaErrorInvalidDevice;
         void *ctx = current_context();
-        if (ctx == nullptr || cache->large.ctx[dev].load(std::memory_order_acquire) != ctx) {
+        bool fits = ctx != nullptr && cache->large.ctx[dev].load(std::memory_order_acquire) == ctx;
+        if (!fits) {
             e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             if (e != cudaSuccess) return e;
-            int fit = 0;
-            if (cudaOccupancyMaxActiveClusters(&fit, fn, &cfg) == cudaSuccess && fit > 0) {
-                cache->large.ctx[dev].store(current_context(), std::memory_order_release);
-            } else {
-                (void)cudaGetLastError();
-                at[0].val.clusterDim.x = kCluster;
-                cfg.gridDim = dim3(kCluster);
-            }
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim.x = kClusterLarge;
+            at[0].val.clusterDim.y = 1;
+            at[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(kClusterLarge);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = (size_t)smem_max;
+            cfg.attrs = at;
+            cfg.numAttrs = 1;
+            int n = 0;
+            fits = cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess && n > 0;
+            if (fits) cache->large.ctx[dev].store(current_context(), std::memory_order_release);
+            else (void)cudaGetLastError();
         }
+        if (fits) ctas = kClusterLarge;
     }
-    return cudaLaunchKernelEx(&cfg, kern, q);
+    return launch_after(kern, dim3(ctas), kThreads, (size_t)smem, ctas, stream, q);
 }
 
 static bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

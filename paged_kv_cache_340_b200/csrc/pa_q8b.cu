@@ -8,6 +8,7 @@
 
 #include "pa_common.cuh"
 #include "pa_internal.h"
+#include "pa_pdl.cuh"
 
 namespace pa {
 namespace q8b {
@@ -120,6 +121,8 @@ __global__ void __launch_bounds__(kWarps * 32, AppendShape<T, D, BS>::kCtas) app
     using Mag = Magnitude<T>;
     constexpr int kVec = Sh::kVec, kLanes = Sh::kLanes, kRows = Sh::kRows, kIt = Sh::kIt;
     constexpr bool kHold = Sh::kHold;
+    wait_previous();
+    allow_next();
     const int lane = threadIdx.x & 31;
     const int H = p.num_kv_heads;
     const int u = blockIdx.x;
@@ -253,14 +256,9 @@ static cudaError_t launch_append_t(const AppendParams &p, int head_dim, int bloc
     long long per = units * warps_y / (8ll * sm_count());
     per = per < 1 ? 1 : per > 4 ? 4 : per;
     const dim3 grid((unsigned)units, (unsigned)((warps_y + per - 1) / per));
-    if (head_dim == 128) {
-        if (block_size == 16) append_kernel<T, 128, 16><<<grid, kWarps * 32, 0, stream>>>(p);
-        else append_kernel<T, 128, 32><<<grid, kWarps * 32, 0, stream>>>(p);
-    } else {
-        if (block_size == 16) append_kernel<T, 64, 16><<<grid, kWarps * 32, 0, stream>>>(p);
-        else append_kernel<T, 64, 32><<<grid, kWarps * 32, 0, stream>>>(p);
-    }
-    return cudaGetLastError();
+    auto kern = head_dim == 128 ? (block_size == 16 ? append_kernel<T, 128, 16> : append_kernel<T, 128, 32>)
+                                : (block_size == 16 ? append_kernel<T, 64, 16> : append_kernel<T, 64, 32>);
+    return launch_after(kern, grid, kWarps * 32, 0, 1, stream, p);
 }
 
 static bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
