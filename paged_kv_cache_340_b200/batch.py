@@ -15,10 +15,11 @@ from typing import Optional
 import numpy as np
 import torch
 
-from . import (PA_POOL_FIFO, BlockPool, DevicePool, PrefixCache, pa_beam_step, pa_choose_partition, pa_copy_blocks,
-               pa_copy_blocks_counted, pa_copy_blocks_q8, pa_decode, pa_decode_append, pa_decode_q8, pa_decode_splitk,
-               pa_decode_splitk_q8, pa_prefill, pa_reshape_and_cache, pa_reshape_and_cache_q8, pa_splitk_reduce,
-               pa_splitk_workspace_bytes)
+from . import (PA_POOL_FIFO, BlockPool, DevicePool, PrefixCache, pa_append_q8b, pa_beam_step, pa_choose_partition,
+               pa_copy_blocks, pa_copy_blocks_counted, pa_copy_blocks_q8, pa_copy_blocks_q8b, pa_decode, pa_decode_append,
+               pa_decode_q8, pa_decode_q8b, pa_decode_q8b_workspace_bytes, pa_decode_splitk, pa_decode_splitk_q8,
+               pa_dpool_append, pa_dpool_release, pa_prefill, pa_reshape_and_cache, pa_reshape_and_cache_q8,
+               pa_splitk_reduce, pa_splitk_workspace_bytes)
 from .workloads import Spec
 
 
@@ -468,6 +469,71 @@ class HostStepPipeline:
         for j in range(2):
             if self.i > j:
                 comp.wait_event(self.out_free[j])
+
+
+class ServingStep:
+    """Continuous batching with the whole step on the device, over an int8
+    cache with one scale per (block, kv head).
+
+    num_seqs rows hold the running sequences (a row without one has length 0).
+    A step frees the rows marked finished, appends new_lens[s] tokens to each
+    row (a prompt, one decoded token, or none), copies the shared blocks it
+    writes into, writes the new K/V rows and decodes every row's last token:
+    the host neither allocates blocks nor reads anything back, and every
+    buffer keeps its size, so a step can be captured in a CUDA graph once and
+    replayed. Its calls go to one stream; steps of one object must not overlap.
+
+    A prompt's row is decoded for its last token like any other; rows of
+    length 0 give zeros. Check pa_read_device_errors() now and then: a step
+    that the pool has no room for appends nothing (q_start is all 0)."""
+
+    def __init__(self, num_seqs: int, max_blocks_per_seq: int, num_blocks: int, block_size: int, num_heads: int,
+                 num_kv_heads: int, head_dim: int, max_tokens: int, dtype: torch.dtype = torch.bfloat16,
+                 out_dtype: Optional[torch.dtype] = None, scale: Optional[float] = None, policy: int = PA_POOL_FIFO,
+                 device="cuda", pool: Optional[DevicePool] = None):
+        i32 = dict(dtype=torch.int32, device=device)
+        self.pool = pool if pool is not None else DevicePool(num_blocks, block_size, policy, device=device)
+        self.block_tables = torch.full((num_seqs, max_blocks_per_seq), -1, **i32)
+        self.context_lens = torch.zeros(num_seqs, **i32)
+        self.q_start = torch.zeros(num_seqs + 1, **i32)
+        self.slot_mapping = torch.empty(max_tokens, **i32)
+        self.cow_pairs = torch.empty((num_seqs, 2), dtype=torch.int64, device=device)
+        self.num_cow = torch.zeros(1, **i32)
+        shape = (num_blocks, num_kv_heads, block_size, head_dim)
+        self.k_cache = torch.zeros(shape, dtype=torch.int8, device=device)
+        self.v_cache = torch.zeros(shape, dtype=torch.int8, device=device)
+        self.k_scale = torch.zeros(shape[:2], dtype=torch.float32, device=device)
+        self.v_scale = torch.zeros(shape[:2], dtype=torch.float32, device=device)
+        self.max_context_len = max_blocks_per_seq * block_size
+        nbytes = pa_decode_q8b_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, self.max_context_len)
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.out = torch.empty((num_seqs, num_heads, head_dim), dtype=out_dtype or dtype, device=device)
+        self.scale = head_dim ** -0.5 if scale is None else scale
+
+    def cache(self) -> tuple:
+        return self.k_cache, self.v_cache, self.k_scale, self.v_scale
+
+    def schedule(self, new_lens, finished, stream=None) -> None:
+        """The step's pool work: finished rows freed, new tokens given their
+        blocks and slots, shared blocks copied (new_lens and finished: device
+        int32 [num_seqs])."""
+        pa_dpool_release(self.pool, self.block_tables, self.context_lens, finished, stream=stream)
+        pa_dpool_append(self.pool, self.block_tables, self.context_lens, new_lens, self.q_start, self.slot_mapping,
+                        self.cow_pairs, self.num_cow, stream=stream)
+        pa_copy_blocks_q8b(*self.cache(), self.cow_pairs, self.num_cow, stream=stream)
+
+    def attend(self, key, value, query, stream=None) -> torch.Tensor:
+        """One layer's part: key and value [max_tokens, Hkv, D] (the new tokens
+        row after row, then padding) into the cache, then the attention of
+        query [num_seqs, Hq, D], each row's last token. Returns out."""
+        pa_append_q8b(key, value, self.q_start, *self.cache(), self.block_tables, self.context_lens, stream=stream)
+        pa_decode_q8b(self.out, query, *self.cache(), self.block_tables, self.context_lens, self.scale,
+                      self.max_context_len, self.workspace, stream=stream)
+        return self.out
+
+    def step(self, new_lens, finished, key, value, query, stream=None) -> torch.Tensor:
+        self.schedule(new_lens, finished, stream)
+        return self.attend(key, value, query, stream)
 
 
 @dataclass
