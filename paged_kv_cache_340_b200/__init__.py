@@ -195,10 +195,10 @@ def _addr(t: torch.Tensor, dtype: torch.dtype, device: int) -> int:
     return t.data_ptr()
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, device: int = -1) -> Optional[int]:
     if stream is None:
         # torch.cuda.current_stream().cuda_stream without the Stream object (0.3 us instead of 3.3)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(device if device >= 0 else torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -481,8 +481,9 @@ def pa_dpool_append(pool: DevicePool, block_tables, context_lens, new_lens, q_st
                               _addr(block_tables, i32, dev), MB, _addr(context_lens, i32, dev),
                               _addr(new_lens, i32, dev), S, _addr(q_start, i32, dev), _addr(slot_mapping, i32, dev),
                               slot_mapping.shape[0], _addr(cow_pairs, torch.int64, dev), _addr(num_cow, i32, dev),
-                              _stream(stream))
-    _check(rc, "pa_dpool_append")
+                              _stream(stream, dev))
+    if rc:
+        _check(rc, "pa_dpool_append")
 
 
 def pa_dpool_release(pool: DevicePool, block_tables, context_lens, finished, stream=None) -> None:
@@ -494,8 +495,9 @@ def pa_dpool_release(pool: DevicePool, block_tables, context_lens, finished, str
     dev, i32 = torch.cuda.current_device(), torch.int32
     rc = _lib.pa_dpool_release(_addr(pool.state, i32, dev), pool.num_blocks, pool.block_size,
                                _addr(block_tables, i32, dev), MB, _addr(context_lens, i32, dev),
-                               _addr(finished, i32, dev), S, _stream(stream))
-    _check(rc, "pa_dpool_release")
+                               _addr(finished, i32, dev), S, _stream(stream, dev))
+    if rc:
+        _check(rc, "pa_dpool_release")
 
 
 # ------------------------------------- int8 caches with a scale per block
@@ -524,8 +526,9 @@ def pa_append_q8b(key, value, q_start, k_cache, v_cache, k_scale, v_scale, block
     rc = _lib.pa_append_q8b(_addr(key, src, dev), _addr(value, src, dev), _dtype(key), _addr(q_start, i32, dev), T,
                             _addr(k_cache, i8, dev), _addr(v_cache, i8, dev), _addr(k_scale, f32, dev),
                             _addr(v_scale, f32, dev), _addr(block_tables, i32, dev), MB,
-                            _addr(context_lens, i32, dev), S, NB, Hkv, D, bs, _stream(stream))
-    _check(rc, "pa_append_q8b")
+                            _addr(context_lens, i32, dev), S, NB, Hkv, D, bs, _stream(stream, dev))
+    if rc:
+        _check(rc, "pa_append_q8b")
 
 
 def pa_decode_q8b_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len) -> int:
@@ -557,8 +560,9 @@ def pa_decode_q8b(out, query, k_cache, v_cache, k_scale, v_scale, block_tables, 
                             _addr(k_cache, i8, dev), _addr(v_cache, i8, dev), _addr(k_scale, f32, dev),
                             _addr(v_scale, f32, dev), _addr(block_tables, i32, dev), MB,
                             _addr(context_lens, i32, dev), S, Hq, Hkv, D, scale, bs, NB, max_context_len, _dtype(out),
-                            order, ws, nbytes, _stream(stream))
-    _check(rc, "pa_decode_q8b")
+                            order, ws, nbytes, _stream(stream, dev))
+    if rc:
+        _check(rc, "pa_decode_q8b")
 
 
 def pa_copy_blocks_q8b(k_cache, v_cache, k_scale, v_scale, src_dst_pairs, num_pairs=None, stream=None) -> None:
@@ -572,8 +576,9 @@ def pa_copy_blocks_q8b(k_cache, v_cache, k_scale, v_scale, src_dst_pairs, num_pa
     rc = _lib.pa_copy_blocks_q8b(_addr(k_cache, i8, dev), _addr(v_cache, i8, dev), _addr(k_scale, f32, dev),
                                  _addr(v_scale, f32, dev), _addr(src_dst_pairs, torch.int64, dev),
                                  None if num_pairs is None else _addr(num_pairs, torch.int32, dev), n, NB, Hkv, D, bs,
-                                 _stream(stream))
-    _check(rc, "pa_copy_blocks_q8b")
+                                 _stream(stream, dev))
+    if rc:
+        _check(rc, "pa_copy_blocks_q8b")
 
 
 def pa_read_device_errors(stream=None) -> int:
