@@ -37,8 +37,11 @@ template <typename T, int D, int BS> struct AppendShape {
     static constexpr int kVec = 16 / sizeof(T);  // values of a lane's vector
     static constexpr int kLanes = D / kVec;      // lanes of a row
     static constexpr int kRows = 32 / kLanes;    // rows per warp load
-    static constexpr int kIt = BS / kRows;       // loads per full block
-    static constexpr bool kHold = kIt <= 16;     // 4 kIt registers hold the rows
+    // warps that share a block, so that its rows take at most 64 registers of a
+    // lane (a warp alone with 128 took 143 us where the pair takes 109: prompts
+    // of 2048 fp32 tokens, 32 heads of 128, blocks of 32)
+    static constexpr int kTeam = BS / kRows > 16 ? 2 : 1;
+    static constexpr int kIt = BS / kRows / kTeam;  // loads of a warp per full block
     static constexpr int kCtas = kIt <= 8 ? 4 : 3;
 };
 
@@ -110,17 +113,15 @@ template <typename T> struct Magnitude {
 
 // One CTA per unit and part of the heads, one warp per (head, K or V) at a
 // time, 16 bytes a lane. The block's rows stay in registers between the search
-// for the largest value and the quantization (unless they take over 64 of
-// them), so HBM sees each byte once; about 4 instructions a value leave the
-// loads the bound (a first version with conversions, clamps and one (head, K or
-// V) per warp took 99 us where this one takes 67 for 2048-token prompts of 32
-// heads, 403 MB).
+// for the largest value and the quantization, so HBM sees each byte once; about
+// 4 instructions a value leave the loads the bound (a first version with
+// conversions and clamps and one (head, K or V) a warp took 99 us where this
+// one takes 67 for eight fp16 prompts of 2048 tokens and 32 heads, 403 MB).
 template <typename T, int D, int BS>
 __global__ void __launch_bounds__(kWarps * 32, AppendShape<T, D, BS>::kCtas) append_kernel(const AppendParams p) {
     using Sh = AppendShape<T, D, BS>;
     using Mag = Magnitude<T>;
-    constexpr int kVec = Sh::kVec, kLanes = Sh::kLanes, kRows = Sh::kRows, kIt = Sh::kIt;
-    constexpr bool kHold = Sh::kHold;
+    constexpr int kVec = Sh::kVec, kLanes = Sh::kLanes, kRows = Sh::kRows, kIt = Sh::kIt, kTeam = Sh::kTeam;
     wait_previous();
     allow_next();
     const int lane = threadIdx.x & 31;
@@ -144,8 +145,22 @@ __global__ void __launch_bounds__(kWarps * 32, AppendShape<T, D, BS>::kCtas) app
         return;
     }
     const int o0 = a - lb * BS, n = e - a;  // the new rows are slots o0 .. o0 + n - 1 of the block
-    const int row = lane / kLanes, col = (lane % kLanes) * kVec;
-    for (int which = blockIdx.y * kWarps + (threadIdx.x >> 5); which < 2 * H; which += gridDim.y * kWarps) {
+    const int warp = threadIdx.x >> 5, part = warp % kTeam;
+    const int row = part * kIt * kRows + lane / kLanes, col = (lane % kLanes) * kVec;
+    // the largest of the team's warps; two slots a warp, used in turn
+    __shared__ uint32_t team_mag[2][kWarps];
+    int turn = 0;
+    auto over_team = [&](uint32_t m) -> uint32_t {
+        if constexpr (kTeam > 1) {
+            if (lane == 0) team_mag[turn][warp] = m;
+            named_bar_sync(1 + warp / kTeam, kTeam * 32);
+            m = max(team_mag[turn][warp], team_mag[turn][warp ^ 1]);
+            turn ^= 1;
+        }
+        return m;
+    };
+    constexpr int kTeams = kWarps / kTeam;
+    for (int which = blockIdx.y * kTeams + warp / kTeam; which < 2 * H; which += gridDim.y * kTeams) {
         const int h = which >> 1;
         const bool is_v = which & 1;
         const T *src = static_cast<const T *>(is_v ? p.value : p.key) + ((size_t)(q0 + a - p0) * H + h) * D + col;
@@ -157,34 +172,28 @@ __global__ void __launch_bounds__(kWarps * 32, AppendShape<T, D, BS>::kCtas) app
             const int r = i * kRows + row;
                         return r < n ? __ldg(reinterpret_cast<const uint4 *>(src + (size_t)r * H * D)) : make_uint4(0u, 0u, 0u, 0u);
         };
-        uint4 held[kHold ? kIt : 1];
+        uint4 held[kIt];
         uint32_t mag = 0;
-        if constexpr (kHold) {
 #pragma unroll
-            for (int i = 0; i < kIt; ++i) held[i] = load(i);
-        }
+        for (int i = 0; i < kIt; ++i) held[i] = load(i);
 #pragma unroll
         for (int i = 0; i < kIt; ++i) {
-            uint4 v;
-            if constexpr (kHold) v = held[i];
-            else v = load(i);
-            mag = Mag::larger(Mag::larger(mag, v.x), v.y);
-            mag = Mag::larger(Mag::larger(mag, v.z), v.w);
+            mag = Mag::larger(Mag::larger(mag, held[i].x), held[i].y);
+            mag = Mag::larger(Mag::larger(mag, held[i].z), held[i].w);
         }
-        mag = Mag::over_warp(mag);
-        const bool finite = mag < Mag::kInf;  // the same in the whole warp
+        mag = over_team(Mag::over_warp(mag));
+        const bool finite = mag < Mag::kInf;  // the same in the whole team
         float amax = Mag::value(mag);
         if (!finite) {  // rare: the largest finite value instead
             amax = 0.f;
 #pragma unroll
             for (int i = 0; i < kIt; ++i) {
                 float x[kVec];
-                if constexpr (kHold) Elt<T>::unpack(held[i], x);
-                else Elt<T>::unpack(load(i), x);
+                Elt<T>::unpack(held[i], x);
 #pragma unroll
                 for (int c = 0; c < kVec; ++c) amax = fabsf(x[c]) <= FLT_MAX ? fmaxf(amax, fabsf(x[c])) : amax;
             }
-            amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+            amax = __uint_as_float(over_team(__reduce_max_sync(0xffffffffu, __float_as_uint(amax))));
         }
         float now = __fdiv_rn(amax, 127.f);
         if (now < FLT_MIN) now = 0.f;
@@ -195,8 +204,7 @@ __global__ void __launch_bounds__(kWarps * 32, AppendShape<T, D, BS>::kCtas) app
             const int r = i * kRows + row;
             if (r >= n) continue;
             float x[kVec];
-            if constexpr (kHold) Elt<T>::unpack(held[i], x);
-            else Elt<T>::unpack(load(i), x);
+            Elt<T>::unpack(held[i], x);
             uint32_t w[kVec / 4];
 #pragma unroll
             for (int c = 0; c < kVec; c += 4) {
@@ -213,10 +221,10 @@ __global__ void __launch_bounds__(kWarps * 32, AppendShape<T, D, BS>::kCtas) app
             else *reinterpret_cast<uint32_t *>(d) = w[0];
         }
         if (now > old) {
-            if (lane == 0) *scale = now;
+            if (lane == 0 && part == 0) *scale = now;
             if (o0 > 0) {  // the older rows' codes in the raised scale
                 const float ratio = __fdiv_rn(old, now);
-                for (int i = lane; i < o0 * D / 4; i += 32) {
+                for (int i = part * 32 + lane; i < o0 * D / 4; i += 32 * kTeam) {
                     uint32_t w = reinterpret_cast<uint32_t *>(dst)[i], r = 0;
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
@@ -224,7 +232,7 @@ __global__ void __launch_bounds__(kWarps * 32, AppendShape<T, D, BS>::kCtas) app
                     reinterpret_cast<uint32_t *>(dst)[i] = r;
                 }
             }
-        } else if (o0 == 0 && lane == 0) {
+        } else if (o0 == 0 && lane == 0 && part == 0) {
             *scale = now;  // a fresh block of zeros
         }
     }
@@ -253,7 +261,8 @@ static cudaError_t launch_append_t(const AppendParams &p, int head_dim, int bloc
     // (head, K or V) pairs a warp takes one after another: two where 8 CTAs
     // an SM are left, which halves the lookups (1, 2, 3 and 4 took 69.4, 67.0,
     // 66.5 and 67.5 us for prompts of 2048 tokens and 32 heads)
-    const int warps_y = (2 * p.num_kv_heads + kWarps - 1) / kWarps;
+    const int team = sizeof(T) == 4 && head_dim == 128 && block_size == 32 ? AppendShape<float, 128, 32>::kTeam : 1;
+    const int warps_y = (2 * p.num_kv_heads * team + kWarps - 1) / kWarps;
     long long per = units * warps_y / (8ll * sm_count());
     per = per < 1 ? 1 : per > 2 ? 2 : per;
     const dim3 grid((unsigned)units, (unsigned)((warps_y + per - 1) / per));
