@@ -675,8 +675,9 @@ int pa_append_q8b(const void *key, const void *value, pa_dtype src_dtype, const 
  * pa_decode_q8b -- pa_decode over that cache: out = softmax(scale q . K_t)
  * V_t with K_t = kq_t * k_scale[block, h], V_t = vq_t * v_scale[block, h].
  * query is q_dtype (PA_F16 or PA_BF16); out_dtype q_dtype or PA_F32.
- * max_context_len bounds every context_lens[s] (longer ones are clamped,
- * PA_DEVERR_CONTEXT). workspace (nullable device buffer, 16-byte aligned, of
+ * max_context_len (at most 2^30) bounds every context_lens[s] (longer ones are
+ * clamped, PA_DEVERR_CONTEXT); the closer the bound, the better the split.
+ * A query row that is not finite gives a NaN output row. workspace (nullable device buffer, 16-byte aligned, of
  * at least pa_decode_q8b_workspace_bytes, else PA_ERR_WORKSPACE) lets a batch
  * of few, long sequences be split along the tokens over more CTAs and joined;
  * without it each (sequence, kv head) is one CTA's work. Its contents need no

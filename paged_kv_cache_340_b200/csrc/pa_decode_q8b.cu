@@ -85,6 +85,7 @@ struct DecodeParams {
     unsigned int *err;
 };
 
+constexpr int kMaxContext = 1 << 30;
 constexpr int kG = 8;                          // query heads per item, at most
 constexpr int kRowBytes = 128;
 constexpr int kTile = 128 * kRowBytes;         // 16 KB of K or V
@@ -1004,7 +1005,8 @@ using namespace pa;
 extern "C" size_t pa_decode_q8b_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                                                 int max_context_len) {
     if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 ||
-        (head_dim != 64 && head_dim != 128) || max_context_len < 0 || num_heads % num_kv_heads != 0 ||
+        (head_dim != 64 && head_dim != 128) || max_context_len < 0 || max_context_len > q8b::kMaxContext ||
+        num_heads % num_kv_heads != 0 ||
         q8b::rows_of(num_heads, num_kv_heads) > 65535)
         return 0;
     const int rows_y = (int)q8b::rows_of(num_heads, num_kv_heads);
@@ -1020,7 +1022,8 @@ extern "C" int pa_decode_q8b(void *out, const void *query, pa_dtype q_dtype, con
                              int num_blocks, int max_context_len, pa_dtype out_dtype, const int32_t *seq_order,
                              void *workspace, size_t workspace_bytes, cudaStream_t stream) {
     if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_blocks < 0 || max_blocks_per_seq < 0 ||
-        num_seqs > 65535 || num_kv_heads > 65535 || max_context_len < 0 || !std::isfinite(scale))
+        num_seqs > 65535 || num_kv_heads > 65535 || max_context_len < 0 || max_context_len > q8b::kMaxContext ||
+        !std::isfinite(scale))
         return PA_ERR_SHAPE;
     if (q_dtype != PA_F16 && q_dtype != PA_BF16) return PA_ERR_DTYPE;
     if (out_dtype != q_dtype && out_dtype != PA_F32) return PA_ERR_DTYPE;

@@ -53,7 +53,7 @@ def test_append_q8b_host_checks(pa, kw, code):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(q_dt=0), -2), (dict(out_dt=2), -2), (dict(D=256), -5), (dict(bs=8), -6), (dict(Hq=7), -4), (dict(S=-1), -3),
-    (dict(L=-1), -3), (dict(scale=float("nan")), -3), (dict(scale=float("inf")), -3),
+    (dict(L=-1), -3), (dict(L=(1 << 30) + 1), -3), (dict(scale=float("nan")), -3), (dict(scale=float("inf")), -3),
     (dict(Hkv=65535, Hq=65535 * 9), -3),         # nine heads to a kv head: two CTAs each, past the grid's second axis
     (dict(nb=1 << 27, Hkv=8), -3),               # cache rows past int32
     (dict(out=None), -1), (dict(q=None), -1), (dict(ks=None), -1), (dict(tables=None), -1),
@@ -70,6 +70,8 @@ def test_decode_q8b_host_checks(pa, kw, code):
 def test_decode_q8b_workspace_bytes(pa):
     f = pa.pa_decode_q8b_workspace_bytes
     assert f(-1, 8, 2, 128, 100) == 0 and f(1, 0, 2, 128, 100) == 0 and f(1, 8, 2, 128, -1) == 0
+    assert f(1, 8, 3, 128, 100) == 0 and f(1, 8, 2, 96, 100) == 0 and f(1, 8, 2, 128, (1 << 30) + 1) == 0
+    assert f(1, 8, 2, 128, 1 << 30) > 0
     for S, Hq, Hkv, D, L in [(0, 8, 8, 64, 0), (1, 8, 8, 128, 1), (8, 32, 8, 128, 131072), (256, 32, 8, 128, 4096)]:
         n = f(S, Hq, Hkv, D, L)
         assert 0 < n < 1 << 28
