@@ -89,19 +89,20 @@ constexpr int kMaxContext = 1 << 30;
 constexpr int kG = 8;                          // query heads per item, at most
 constexpr int kRowBytes = 128;
 constexpr int kTile = 128 * kRowBytes;         // 16 KB of K or V
-constexpr int kStages = 2;
-constexpr int kScales = 4;                     // tiles whose scales are kept: warp 5 is at most three tiles ahead
 constexpr int kClaimAhead = 4;                 // tiles still to be loaded when another item is claimed
 // Splitting along the tokens, in tiles: 16-tile pieces measured best of 8, 12,
 // 16, 32 and 64 for 8 sequences of 32,768 to 131,072 tokens (163, 161, 158, 172, 195 us).
 constexpr int kPiece = 16, kPieceMost = 48;
 constexpr int kMaxBlocks = 16;                 // blocks of a tile, at most
-constexpr int kSoftmaxThreads = 128;
-constexpr int kMmaWarp = 4, kLoadK = 5, kLoadV = 6, kItemWarp = 7;
-constexpr int kThreads = 8 * 32;
+// Virtual heads from which the softmax has two warpgroups: 16 (222 sequences of
+// 4096 tokens, 8 kv heads of 64 with 8 query heads each: 273 -> 227 us); at 8 the
+// third CTA that one warpgroup leaves room for is worth more (151 against 167 us).
+constexpr int kTwoTeams = 16;
 constexpr int kQMax = 8355711;                 // 127 * 65536 + 127 * 256 + 127, three signed digits
 constexpr float kQUnit = 8355711.f;
 constexpr float kWUnit = 16777215.f;           // 2^24 - 1
+constexpr float kNone = -3e38f;                // below every score: the maximum of no tokens
+constexpr float kRaise = 16.f;                 // see the softmax
 
 // An item, as warp 7 hands it to the others.
 struct Item {
@@ -126,8 +127,18 @@ struct Scales {
 // digit rows a product reads past 3 V (up to kN) only give columns that nobody
 // reads, so those rows are whatever lies behind.
 template <int V> struct Shape {
+    // softmax warpgroups: two halve the heads, and so a tile's time, where that bounds
+    static constexpr int kTeams = V >= kTwoTeams ? 2 : 1;
+    static constexpr int kSoftmaxThreads = 128 * kTeams, kThreads = kSoftmaxThreads + 128;
+    static constexpr int kMmaWarp = 4 * kTeams, kLoadK = kMmaWarp + 1, kLoadV = kMmaWarp + 2, kItemWarp = kMmaWarp + 3;
     static constexpr int kN = (3 * V + 15) / 16 * 16;          // MMA columns
-    static constexpr int kItems = V <= 2 ? 4 : V <= 4 ? 3 : 2;  // items known at a time (as shared memory allows)
+    // as shared memory allows: stages of K and of V, items known at a time
+    static constexpr int kStages = kTeams == 2 && V <= 8 ? 3 : 2;
+    static constexpr int kItems = kTeams == 2 ? (V <= 8 ? 3 : 4) : V <= 2 ? 4 : V <= 4 ? 3 : 2;
+    // tiles whose scales are kept: the K warp fills tile t once S of tile t -
+    // kStages is computed, and that was issued after O of the tile two before,
+    // whose scales have been read
+    static constexpr int kScales = kStages + 2;
     static constexpr int kDigits = (3 * V + 7) / 8 * 1024;     // bytes of 3 V digit rows, in 8-row groups
     static constexpr int kOffK = 0;
     static constexpr int kOffV = kOffK + kStages * kTile;
@@ -146,12 +157,11 @@ template <int V> struct Shape {
     // tensor memory: S in two buffers, O in one
     static constexpr int kSCol = 0, kOCol = 2 * kN;
     static constexpr int kCols = 3 * kN <= 64 ? 64 : 3 * kN <= 128 ? 128 : 256;
-    // CTAs per SM: three, by shared memory; two for 16 virtual heads (tensor memory), held to it by registers
-    static constexpr int kCtas = kCols <= 128 ? 3 : 2;
-    // registers: of the launch, and after warps 4-7 have given theirs to warps 0-3
-    static constexpr int kRegs = kCtas == 3 ? 80 : 128;
-    static constexpr int kRegsLow = 40, kRegsHigh = kCtas == 3 ? 120 : 216;
-    static_assert(kRegsLow + kRegsHigh <= 2 * kRegs, "registers taken over are registers given up");
+    // CTAs per SM: three, by shared memory; two with two softmax warpgroups
+    static constexpr int kCtas = kTeams == 1 ? 3 : 2;
+    // registers: of the launch, and after the last four warps have given theirs to the softmax
+    static constexpr int kRegs = 80, kRegsLow = 40, kRegsHigh = kTeams == 1 ? 120 : 96;
+    static_assert(kRegsLow + kTeams * kRegsHigh <= (kTeams + 1) * kRegs, "registers taken over are registers given up");
     static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "CTAs per SM");
     static_assert(kCtas * kCols <= 512 && (kCtas + 1) * kRegs * kThreads > 65536, "tensor memory for every resident CTA");
     static_assert(8 * V * 4 + (V > 1 ? V / 2 : 1) * 64 * 4 <= kDigits, "the threads' sums fit the weights' digits");
@@ -219,8 +229,8 @@ template <int kC> __device__ __forceinline__ void tmem_load(uint32_t addr, int (
     for (int i = 0; i < kC; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// Barrier over the softmax threads; true in all of them when `v` holds in all of them.
-__device__ __forceinline__ bool softmax_sync_and(bool v) {
+// Barrier over the N softmax threads; true in all of them when `v` holds in all of them.
+template <int N> __device__ __forceinline__ bool sync_and(bool v) {
     uint32_t all;
     asm volatile(
         "{\n\t.reg .pred pv, pa;\n\t"
@@ -228,7 +238,7 @@ __device__ __forceinline__ bool softmax_sync_and(bool v) {
         "barrier.cta.red.and.pred pa, 1, %2, pv;\n\t"
         "selp.u32 %0, 1, 0, pa;\n\t}"
         : "=r"(all)
-        : "r"((uint32_t)v), "n"(kSoftmaxThreads)
+        : "r"((uint32_t)v), "n"(N)
         : "memory");
     return all != 0;
 }
@@ -251,6 +261,14 @@ template <int N, int Mask> __device__ __forceinline__ void warp_sums(float *x, i
             warp_sums<1, Mask / 2>(x, lane);
         }
     }
+}
+
+// The number whose base-256 digits' sums are hi, mid and lo (each below 2^22 in
+// magnitude). One conversion instruction instead of two: they are issued at an
+// eighth of the rate of sums. The first goes by adding 1.5 * 2^23 as bits.
+__device__ __forceinline__ float number(int hi, int mid, int lo) {
+    const float h = __int_as_float(0x4b400000 + hi) - 12582912.f;
+    return fmaf(h, 65536.f, (float)(mid * 256 + lo));
 }
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -307,15 +325,17 @@ __device__ __forceinline__ bool canceled(const void *answer, int &x, int &y, int
 // ------------------------------------------------------------------- kernel
 
 template <typename T, int D, int G>
-__global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
+__global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128 / D)>::kCtas)
     decode_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                   const DecodeParams p) {
     constexpr int kPar = 128 / D;   // tokens per row
     constexpr int kV = G * kPar;    // virtual heads: par * G + g
     using Sh = Shape<kV>;
-    constexpr int kN = Sh::kN;
-    constexpr int kCols3 = (3 * kV + 3) / 4 * 4;  // S columns read: three a virtual head
-    constexpr int kOCols3 = (3 * G + 3) / 4 * 4;  // O columns read: those of the lane's own tokens
+    constexpr int kN = Sh::kN, kStages = Sh::kStages, kScales = Sh::kScales, kTeams = Sh::kTeams;
+    constexpr int kSoftmaxThreads = Sh::kSoftmaxThreads, kMmaWarp = Sh::kMmaWarp, kLoadV = Sh::kLoadV;
+    constexpr int kSV = kV / kTeams, kOG = G / kTeams;  // virtual heads of a softmax thread, and heads whose O it adds up
+    constexpr int kCols3 = (3 * kSV + 3) / 4 * 4;  // S columns read: three a virtual head
+    constexpr int kOCols3 = (3 * kOG + 3) / 4 * 4; // O columns read: those of the lane's own tokens
     constexpr int kTok = 128 * kPar;              // tokens per tile
     constexpr int kItems = Sh::kItems;
 
@@ -370,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
         for (int i = 0; i < kItems; ++i) {
             mbar_init(i_full + i, 1);
             mbar_init(q_full + i, 1);
-            mbar_init(i_empty + i, 7);  // warps 0-6
+            mbar_init(i_empty + i, 4 * kTeams + 3);  // every warp but the item warp
         }
         *abort_flag = 0;
         *loaded = 0;
@@ -389,9 +409,9 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
     wait_previous();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp >= 4) {
+    if (warp >= kMmaWarp) {
         regs_dec<Sh::kRegsLow>();
-        if (warp == kItemWarp) {
+        if (warp == Sh::kItemWarp) {
             // ======================================================= item warp
             int x = blockIdx.x, y = blockIdx.y, z = blockIdx.z;
             bool more = true, sound = true;
@@ -542,7 +562,6 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
         } else if (warp != kMmaWarp) {
             // ======================================================= load warps
             // Lane i brings block i of the tile: `rows` rows of 128 bytes.
-            static_assert(kLoadK + 1 == kLoadV, "two load warps");
             const bool is_v = warp == kLoadV;
             const CUtensorMap *map = is_v ? &v_map : &k_map;
             uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
@@ -677,20 +696,22 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
     } else {
         // =================================================== softmax warps
         regs_inc<Sh::kRegsHigh>();
-        const int r = tid;
-        const uint32_t tlane = tmem + ((uint32_t)(warp * 32) << 16);
-        const int block = r / rows;                        // this row's block within a tile
-        const int par0 = kPar == 2 ? (warp >> 1) * G : 0;  // first virtual head of this lane's head dim
+        const int r = tid & 127, quarter = warp & 3;
+        const uint32_t tlane = tmem + ((uint32_t)(quarter * 32) << 16);
+        const int block = r / rows;                           // this row's block within a tile
+        const int v0 = (warp >> 2) * kSV;                     // this thread's first virtual head,
+        const int g0 = (warp >> 2) * kOG;                     // its first head in O,
+        const int vo = (kPar == 2 ? (quarter >> 1) * G : 0) + g0;  // and that one's virtual head (of the lane's head dim)
         float *red_m = reinterpret_cast<float *>(Ps), *red_l = red_m + 4 * kV;
         float *red_o = red_l + 4 * kV;  // [G][64]: the odd tokens' sums at head_dim 64
         int t = 0;                      // tiles done, over all items
-        // The four warps leave the loops together: one whose wait ran out says
-        // so at the next barrier of all four.
+        // The warps leave the loops together: one whose wait ran out says so at
+        // the next barrier of all.
         bool ok = true;
         for (int n = 0; ok; ++n) {
             const int slot = n % kItems;
             bool sound = __all_sync(0xffffffffu, mbar_wait(q_full + slot, (n / kItems) & 1) && !*abort_flag);
-            ok = softmax_sync_and(sound);
+            ok = sync_and<kSoftmaxThreads>(sound);
             if (!ok) break;
             const Item &it = items[slot];
             const int ntiles = it.ntiles;
@@ -698,32 +719,32 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
             const int L = it.end, first = it.first, part = it.part, write = it.write;
             const size_t row0 = (size_t)it.s * p.num_heads + it.head0;  // output row of head 0
             const int g_valid = min(G, p.group - it.head0 % p.group / kG * kG);
-            float qs[kV];
+            float qs[kSV];
 #pragma unroll
-            for (int v = 0; v < kV; ++v) qs[v] = qscale[slot * kV + v];
-            float m_l[kV], l[kV];            // this thread's tokens: largest score, sum of 2^(score - it)
-            float m_o[G], o[G], m_tile[G];   // O of the lane's dim: sum * 2^-m_o; the unit of the tile in tensor memory
+            for (int v = 0; v < kSV; ++v) qs[v] = qscale[slot * kV + v0 + v];
+            float m_l[kSV], l[kSV];                // this thread's tokens: about their largest score, sum of 2^(score - it)
+            float m_o[kOG], o[kOG], m_tile[kOG];   // O of the lane's dim: sum * 2^-m_o; the unit of the tile in tensor memory
 #pragma unroll
-            for (int v = 0; v < kV; ++v) {
-                m_l[v] = -INFINITY;
+            for (int v = 0; v < kSV; ++v) {
+                m_l[v] = kNone;
                 l[v] = 0.f;
             }
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                m_o[g] = m_tile[g] = -INFINITY;
+            for (int g = 0; g < kOG; ++g) {
+                m_o[g] = m_tile[g] = kNone;
                 o[g] = 0.f;
             }
             // adds the tile in tensor memory (its O columns, in units of 2^m_tile / kWUnit) to o
             auto add_tile = [&]() {
                 int c[kOCols3];
-                tmem_load<kOCols3>(tlane + Sh::kOCol + 3 * par0, c);
+                tmem_load<kOCols3>(tlane + Sh::kOCol + 3 * vo, c);
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const float f = fmaf((float)c[3 * g], 65536.f, (float)(c[3 * g + 1] * 256 + c[3 * g + 2]));
+                for (int g = 0; g < kOG; ++g) {
+                    const float f = number(c[3 * g], c[3 * g + 1], c[3 * g + 2]);
                     if (m_tile[g] > m_o[g]) {  // the same in every thread of the warp
-                        o[g] = o[g] * fast_exp2(m_o[g] - m_tile[g]) + f;
+                        o[g] = fmaf(o[g], fast_exp2(m_o[g] - m_tile[g]), f);
                         m_o[g] = m_tile[g];
-                    } else if (m_tile[g] > -INFINITY) {
+                    } else {
                         o[g] = fmaf(f, fast_exp2(m_tile[g] - m_o[g]), o[g]);
                     }
                 }
@@ -731,72 +752,102 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
             for (int j = 0; j < ntiles; ++j, ++t) {
                 float *wm = wmax + (t & 1) * 4 * kV;
                 sound = __all_sync(0xffffffffu, sound && mbar_wait(s_full + (t & 1), (t >> 1) & 1) && !*abort_flag);
-                float x[kV];  // log2 of the weight
+                float x[kSV];  // log2 of the weight
                 if (sound) {
                     fence_after();
                     const Scales &sc = scales[t % kScales];
                     const float ks = sc.k[block], vs = sc.v[block];
-                    const bool valid = (sc.valid >> block) & 1u;
+                    const unsigned valid = sc.valid;
                     const float lv = vs > 0.f ? log2f(vs) : -INFINITY;
                     const int tok = first + j * kTok + r * kPar;
+                    // (the same in every thread)
+                    const bool whole = first + (j + 1) * kTok <= L && valid == (1u << blocks) - 1u;
                     int c[kCols3];
-                    tmem_load<kCols3>(tlane + Sh::kSCol + (t & 1) * kN, c);
+                    tmem_load<kCols3>(tlane + Sh::kSCol + (t & 1) * kN + 3 * v0, c);
+                    float score[kSV];
 #pragma unroll
-                    for (int v = 0; v < kV; ++v) {
-                        const float f = fmaf((float)c[3 * v], 65536.f, (float)(c[3 * v + 1] * 256 + c[3 * v + 2]));
-                        const float score = f * (qs[v] * ks);
-                        const bool live = valid && tok + v / G < L;
-                        if (live) {
-                            const float d = score - m_l[v];
-                            const float e = fast_exp2(-fabsf(d));
-                            l[v] = d > 0.f ? fmaf(l[v], e, 1.f) : l[v] + e;
-                            m_l[v] = fmaxf(m_l[v], score);
-                        }
-                        x[v] = live ? score + lv : -INFINITY;
+                    for (int v = 0; v < kSV; ++v)
+                        score[v] = number(c[3 * v], c[3 * v + 1], c[3 * v + 2]) * (qs[v] * ks);
+                    if (!whole) {
+#pragma unroll
+                        for (int v = 0; v < kSV; ++v)
+                            if (!(valid >> block & 1u) || tok + (v0 + v) / G >= L) score[v] = -INFINITY;
+                    }
+                    // The sum's reference is a score seen before, raised only when one is
+                    // above it by kRaise: a term is then at most 2^kRaise.
+                    float above = -INFINITY;
+#pragma unroll
+                    for (int v = 0; v < kSV; ++v) above = fmaxf(above, score[v] - m_l[v]);
+                    if (above > kRaise) {
+#pragma unroll
+                        for (int v = 0; v < kSV; ++v)
+                            if (score[v] - m_l[v] > kRaise) {
+                                l[v] *= fast_exp2(m_l[v] - score[v]);
+                                m_l[v] = score[v];
+                            }
+                    }
+#pragma unroll
+                    for (int v = 0; v < kSV; ++v) {
+                        l[v] += fast_exp2(score[v] - m_l[v]);
+                        x[v] = score[v] + lv;
                     }
                     // the tile's largest weight per head, over this warp
 #pragma unroll
-                    for (int v = 0; v < kV; ++v) {
+                    for (int v = 0; v < kSV; ++v) {
                         const float mw = warp_max(x[v]);
-                        if (lane == 0) wm[warp * kV + v] = mw;
+                        if (lane == 0) wm[quarter * kV + v0 + v] = mw;
                     }
                 }
-                ok = softmax_sync_and(sound);
+                ok = sync_and<kSoftmaxThreads>(sound);
                 if (!ok) break;
-                float mt[kV];
-                if constexpr (kV % 4 == 0) {
+                // over the four quarters of the tile: N heads from virtual head v on
+                auto tile_max = [&]<int N>(float (&m)[N], int v) {
+                    if constexpr (N % 4 == 0) {
 #pragma unroll
-                    for (int v = 0; v < kV; v += 4) {
-                        float4 w[4];
+                        for (int i = 0; i < N; i += 4) {
+                            float4 w[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4 *>(wm + i * kV + v);
-                        mt[v] = fmaxf(fmaxf(w[0].x, w[1].x), fmaxf(w[2].x, w[3].x));
-                        mt[v + 1] = fmaxf(fmaxf(w[0].y, w[1].y), fmaxf(w[2].y, w[3].y));
-                        mt[v + 2] = fmaxf(fmaxf(w[0].z, w[1].z), fmaxf(w[2].z, w[3].z));
-                        mt[v + 3] = fmaxf(fmaxf(w[0].w, w[1].w), fmaxf(w[2].w, w[3].w));
+                            for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const float4 *>(wm + k * kV + v + i);
+                            m[i] = fmaxf(fmaxf(w[0].x, w[1].x), fmaxf(w[2].x, w[3].x));
+                            m[i + 1] = fmaxf(fmaxf(w[0].y, w[1].y), fmaxf(w[2].y, w[3].y));
+                            m[i + 2] = fmaxf(fmaxf(w[0].z, w[1].z), fmaxf(w[2].z, w[3].z));
+                            m[i + 3] = fmaxf(fmaxf(w[0].w, w[1].w), fmaxf(w[2].w, w[3].w));
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < N; ++i)
+                            m[i] = fmaxf(fmaxf(wm[v + i], wm[kV + v + i]), fmaxf(wm[2 * kV + v + i], wm[3 * kV + v + i]));
                     }
-                } else {
+                };
+                float mt[kSV];
+                tile_max(mt, v0);
 #pragma unroll
-                    for (int v = 0; v < kV; ++v)
-                        mt[v] = fmaxf(fmaxf(wm[v], wm[kV + v]), fmaxf(wm[2 * kV + v], wm[3 * kV + v]));
-                }
+                for (int v = 0; v < kSV; ++v) mt[v] = fmaxf(mt[v], kNone);  // finite, though the weights all be 0
                 if (j > 0) {  // O of the tile before is there: P and O are free once it is added up
                     sound = __all_sync(0xffffffffu, mbar_wait(o_full, (t - 1) & 1) && !*abort_flag);
                     if (!sound) continue;  // (the next barrier tells the others)
                     fence_after();
                     add_tile();
                 }
+                if constexpr (kTeams == 1 && kPar == 1) {
 #pragma unroll
-                for (int g = 0; g < G; ++g) m_tile[g] = kPar == 2 && par0 ? mt[kV - G + g] : mt[g];
+                    for (int g = 0; g < kOG; ++g) m_tile[g] = mt[g];
+                } else {
+                    tile_max(m_tile, vo);
+#pragma unroll
+                    for (int g = 0; g < kOG; ++g) m_tile[g] = fmaxf(m_tile[g], kNone);
+                }
                 // ---- the weights' digits, row 3 v + i, byte r of the row (its 16-byte chunks swizzled)
 #pragma unroll
-                for (int v = 0; v < kV; ++v) {
-                    const float w = x[v] > -INFINITY ? fast_exp2(x[v] - mt[v]) : 0.f;
-                    const unsigned u = __float2uint_rn(w * kWUnit);
-                    const int d = 3 * v;
-                    Ps[d * kRowBytes + (r ^ ((d & 7) << 4))] = (unsigned char)(u >> 16);
-                    Ps[(d + 1) * kRowBytes + (r ^ (((d + 1) & 7) << 4))] = (unsigned char)(u >> 8);
-                    Ps[(d + 2) * kRowBytes + (r ^ (((d + 2) & 7) << 4))] = (unsigned char)u;
+                for (int v = 0; v < kSV; ++v) {
+                    const unsigned u = __float2uint_rn(fast_exp2(x[v] - mt[v]) * kWUnit);
+                    const int d = 3 * v, d0 = 3 * v0;  // (3 v0 is a multiple of 8 with two teams, else 0)
+                    static_assert(kTeams == 1 || 3 * kSV % 8 == 0 || kSV == 4, "swizzle phase");
+                    const int ph = kTeams == 1 || 3 * kSV % 8 == 0 ? 0 : d0 & 7;
+                    unsigned char *row = Ps + d0 * kRowBytes;
+                    row[d * kRowBytes + (r ^ (((d + ph) & 7) << 4))] = (unsigned char)(u >> 16);
+                    row[(d + 1) * kRowBytes + (r ^ (((d + 1 + ph) & 7) << 4))] = (unsigned char)(u >> 8);
+                    row[(d + 2) * kRowBytes + (r ^ (((d + 2 + ph) & 7) << 4))] = (unsigned char)u;
                 }
                 fence_proxy_async_smem();
                 fence_before();
@@ -809,43 +860,44 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
                     fence_after();
                     add_tile();
                 }
-                ok = softmax_sync_and(sound);
+                ok = sync_and<kSoftmaxThreads>(sound);
                 if (!ok) break;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(i_empty + slot);
             // ---- the threads' sums, where the weights' digits were (their product is done), and the output
 #pragma unroll
-            for (int v = 0; v < kV; ++v) {
+            for (int v = 0; v < kSV; ++v) {
                 const float mw = warp_max(m_l[v]);
-                if (m_l[v] > -INFINITY) l[v] *= fast_exp2(m_l[v] - mw);
-                if (lane == 0) red_m[warp * kV + v] = mw;
+                l[v] *= fast_exp2(m_l[v] - mw);
+                if (lane == 0) red_m[quarter * kV + v0 + v] = mw;
             }
-            warp_sums<kV, 16>(l, lane);  // lane c * 32 / kV holds head c's
-            if (lane % (32 / kV) == 0) red_l[warp * kV + lane / (32 / kV)] = l[0];
+            warp_sums<kSV, 16>(l, lane);  // lane c * 32 / kSV holds head c's
+            if (lane % (32 / kSV) == 0) red_l[quarter * kV + v0 + lane / (32 / kSV)] = l[0];
             named_bar_sync(1, kSoftmaxThreads);
-            float m[G], sum[G];
+            float m[kOG], sum[kOG];
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                m[g] = -INFINITY;
+            for (int g = 0; g < kOG; ++g) {
+                const float *gm = red_m + g0 + g, *gl = red_l + g0 + g;  // quarter i's, odd tokens' G further
+                m[g] = kNone;
                 sum[g] = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4 * kPar; ++i) m[g] = fmaxf(m[g], red_m[(i & 3) * kV + (i >> 2) * G + g]);
+                for (int i = 0; i < 4 * kPar; ++i) m[g] = fmaxf(m[g], gm[(i & 3) * kV + (i >> 2) * G]);
 #pragma unroll
                 for (int i = 0; i < 4 * kPar; ++i) {
-                    const float mi = red_m[(i & 3) * kV + (i >> 2) * G + g], li = red_l[(i & 3) * kV + (i >> 2) * G + g];
-                    sum[g] += mi > -INFINITY ? li * fast_exp2(mi - m[g]) : li;  // a NaN query's sum is NaN
+                    const float mi = gm[(i & 3) * kV + (i >> 2) * G], li = gl[(i & 3) * kV + (i >> 2) * G];
+                    sum[g] += li * fast_exp2(mi - m[g]);  // (a NaN query's sum is NaN)
                 }
-                o[g] = m_o[g] > -INFINITY ? o[g] * fast_exp2(m_o[g] - m[g]) : 0.f;
-                if (kPar == 2 && r >= D) red_o[g * D + r - D] = o[g];
+                o[g] *= fast_exp2(m_o[g] - m[g]);
+                if (kPar == 2 && r >= D) red_o[(g0 + g) * D + r - D] = o[g];
             }
             if constexpr (kPar == 2) named_bar_sync(1, kSoftmaxThreads);
             if (r < D && write) {
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    if (g >= g_valid) continue;
-                    if constexpr (kPar == 2) o[g] += red_o[g * D + r];
-                    const size_t row = row0 + g;
+                for (int g = 0; g < kOG; ++g) {
+                    if (g0 + g >= g_valid) continue;
+                    if constexpr (kPar == 2) o[g] += red_o[(g0 + g) * D + r];
+                    const size_t row = row0 + g0 + g;
                     if (p.partition_size) {
                         const size_t at = row * p.max_parts + part;
                         p.ws_acc[at * D + r] = o[g] * (1.f / kWUnit);
@@ -861,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G * (128 / D)>::kCtas)
             }
             // (the sums are read before the next weights are written: the next item's first barrier is in between)
         }
-        if (!ok && r == 0) give_up();
+        if (!ok && tid == 0) give_up();
     }
     fence_before();
     __syncthreads();
@@ -895,28 +947,28 @@ template <int D> __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(
     const size_t row = (size_t)s * p.num_heads + blockIdx.x;
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml) + row * p.max_parts;
     const Vec *acc = reinterpret_cast<const Vec *>(p.ws_acc + row * p.max_parts * D) + lane;
-    float m = -INFINITY, l = 0.f, o[kE] = {};
+    float m = kNone, l = 0.f, o[kE] = {};
     for (int i0 = warp; i0 < n; i0 += kJoinWarps * kU) {
         float2 v[kU];
         Vec a[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {  // kU partitions' loads in flight
             const int i = i0 + kJoinWarps * u;
-            v[u] = i < n ? __ldcg(ml + i) : make_float2(-INFINITY, 0.f);
+            v[u] = i < n ? __ldcg(ml + i) : make_float2(kNone, 0.f);
             a[u] = i < n ? __ldcg(acc + (size_t)i * 32) : Vec{};
         }
         float mn = m;
 #pragma unroll
         for (int u = 0; u < kU; ++u) mn = fmaxf(mn, v[u].x);
-        const float r = m > -INFINITY ? fast_exp2(m - mn) : 0.f;
+        const float r = fast_exp2(m - mn);
         l *= r;
 #pragma unroll
         for (int e = 0; e < kE; ++e) o[e] *= r;
         m = mn;
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            const float w = v[u].x > -INFINITY ? fast_exp2(v[u].x - m) : 0.f;
-            l += v[u].x > -INFINITY ? w * v[u].y : v[u].y;  // (a NaN sum stays)
+            const float w = fast_exp2(v[u].x - m);
+            l = fmaf(w, v[u].y, l);  // (a NaN sum stays)
 #pragma unroll
             for (int e = 0; e < kE; ++e) o[e] = fmaf(w, reinterpret_cast<const float *>(&a[u])[e], o[e]);
         }
@@ -930,15 +982,15 @@ template <int D> __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(
     __syncthreads();
     const int d = threadIdx.x;
     if (d >= D) return;
-    float M = -INFINITY;
+    float M = kNone;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, sm_m[w]);
     float num = 0.f, den = 0.f;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
-        const float f = sm_m[w] > -INFINITY ? fast_exp2(sm_m[w] - M) : 0.f;
+        const float f = fast_exp2(sm_m[w] - M);
         num = fmaf(f, sm_o[w][d], num);
-        den += sm_m[w] > -INFINITY ? f * sm_l[w] : sm_l[w];
+        den = fmaf(f, sm_l[w], den);
     }
     store_out(p.out, row * D + d, den != 0.f ? num / den : 0.f, p.out_dtype);
 }
@@ -962,7 +1014,7 @@ static cudaError_t launch_decode_t(const CUtensorMap &km, const CUtensorMap &vm,
     const dim3 grid(p.max_parts, p.num_kv_heads * p.sub_groups, p.num_seqs);
     // blocks that all start at once leave none to take over
     p.steal = (long long)grid.x * grid.y * grid.z > (long long)Sh::kCtas * sm_count();
-    return launch_after(kern, grid, kThreads, Sh::kSmemBytes, 1, stream, km, vm, p);
+    return launch_after(kern, grid, Sh::kThreads, Sh::kSmemBytes, 1, stream, km, vm, p);
 }
 
 template <typename T>
@@ -983,7 +1035,8 @@ static cudaError_t launch_decode(const CUtensorMap &km, const CUtensorMap &vm, c
 static int partition_of(int num_seqs, int rows_y, int group, int head_dim, int max_ctx) {
     const int tok = 128 * (128 / head_dim);
     const long long items = (long long)num_seqs * rows_y, tiles = ((long long)max_ctx + tok - 1) / tok;
-    const long long ctas = (group > 4 && head_dim == 64 ? 2ll : 3ll) * sm_count();
+    const int heads = (group > 4 ? 8 : group > 2 ? 4 : group) * (128 / head_dim);
+    const long long ctas = (heads >= kTwoTeams ? 2ll : 3ll) * sm_count();
     if (items >= ctas || tiles < 2) return 0;
     long long per = (items * tiles + ctas - 1) / ctas;
     if (per > kPieceMost) per = kPiece;
