@@ -693,6 +693,29 @@ int pa_decode_q8b(void *out, const void *query, pa_dtype q_dtype, const int8_t *
                   float scale, int block_size, int num_blocks, int max_context_len, pa_dtype out_dtype,
                   const int32_t *seq_order, void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * pa_decode_q8b_withhold_tile -- pa_decode_q8b (without a workspace) with a
+ * fault planted on the host, for testing the bounded waits; not for
+ * production use. The CTA of sequence `seq`, kv head `kv_head` never asks for
+ * its K tile `tile` (its tokens 128 * tile ..), so the products that need it
+ * wait for data that never comes. After wait_limit_ns (between 1e5 and 1e9;
+ * the library's own bound is 1 s) the CTA's warps give up one after another,
+ * PA_DEVERR_TIMEOUT is recorded, copies in flight land, tensor memory is freed
+ * and the launch ends normally. The outputs of the (sequence, kv head) pairs
+ * that this CTA had taken on are undefined (that pair alone where all pairs
+ * are resident at once), every other output is pa_decode_q8b's. A tile past
+ * the sequence's end withholds nothing. A separate instance of the kernel:
+ * q_dtype PA_F16 (else PA_ERR_DTYPE), head_dim 128 (PA_ERR_HEAD_DIM),
+ * num_heads == num_kv_heads (PA_ERR_HEADS); seq, kv_head, tile or the limit out
+ * of range give PA_ERR_SHAPE.
+ */
+int pa_decode_q8b_withhold_tile(void *out, const void *query, pa_dtype q_dtype, const int8_t *k_cache,
+                                const int8_t *v_cache, const float *k_scale, const float *v_scale,
+                                const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                                int num_seqs, int num_heads, int num_kv_heads, int head_dim, float scale,
+                                int block_size, int num_blocks, int max_context_len, pa_dtype out_dtype, int seq,
+                                int kv_head, int tile, unsigned long long wait_limit_ns, cudaStream_t stream);
+
 /* pa_copy_blocks for that cache: codes and scales of each pair. num_pairs
  * (nullable device int32): only the first *num_pairs of max_pairs pairs, as
  * pa_copy_blocks_counted. */

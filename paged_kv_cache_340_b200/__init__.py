@@ -64,6 +64,7 @@ EXPORTED = (
     "pa_decode_splitk_q8", "pa_copy_blocks_q8", "pa_decode_append", "pa_decode_withhold_stage",
     "pa_prefill_withhold_tile", "pa_beam_step_withhold_arrival", "pa_dpool_append", "pa_dpool_release",
     "pa_append_q8b", "pa_decode_q8b", "pa_decode_q8b_workspace_bytes", "pa_copy_blocks_q8b",
+    "pa_decode_q8b_withhold_tile",
 )
 
 PA_STATIC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -141,6 +142,8 @@ def _load() -> ctypes.CDLL:
         "pa_decode_q8b_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
         "pa_decode_q8b": (i32, [vp, vp, i32, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, f32, i32, i32, i32, i32,
                                 vp, vp, sz, vp]),
+        "pa_decode_q8b_withhold_tile": (i32, [vp, vp, i32, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, f32, i32, i32,
+                                              i32, i32, i32, i32, i32, ctypes.c_ulonglong, vp]),
         "pa_copy_blocks_q8b": (i32, [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp]),
     }
     for name, (res, args) in sig.items():
@@ -563,6 +566,21 @@ def pa_decode_q8b(out, query, k_cache, v_cache, k_scale, v_scale, block_tables, 
                             order, ws, nbytes, _stream(stream, dev))
     if rc:
         _check(rc, "pa_decode_q8b")
+
+
+def pa_decode_q8b_withhold_tile(out, query, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
+                                max_context_len, seq, kv_head, tile, wait_limit_ns, stream=None) -> None:
+    """pa_decode_q8b with the copy of one 128-token K tile of one (sequence, kv
+    head) withheld, so that its bounded waits run out (a test of the timeout
+    path; that head's output is undefined)."""
+    NB, Hkv, bs, _ = _q8b_cache(k_cache, v_cache, k_scale, v_scale)
+    S, Hq, D = query.shape
+    rc = _lib.pa_decode_q8b_withhold_tile(_ptr(out), _ptr(query), _dtype(query), _ptr(k_cache), _ptr(v_cache),
+                                          _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1],
+                                          _ptr(context_lens), S, Hq, Hkv, D, scale, bs, NB, int(max_context_len),
+                                          _dtype(out), int(seq), int(kv_head), int(tile), int(wait_limit_ns),
+                                          _stream(stream))
+    _check(rc, "pa_decode_q8b_withhold_tile")
 
 
 def pa_copy_blocks_q8b(k_cache, v_cache, k_scale, v_scale, src_dst_pairs, num_pairs=None, stream=None) -> None:

@@ -83,6 +83,10 @@ struct DecodeParams {
     float scale_log2;
     pa_dtype out_dtype;
     unsigned int *err;
+    // test hook (pa_decode_q8b_withhold_tile; its own instance of the kernel): the K tile `withhold_tile` of this
+    // (sequence, kv head) is never asked for, and every wait gives up after wait_limit_ns
+    int withhold_seq, withhold_kvh, withhold_tile;
+    unsigned long long wait_limit_ns;
 };
 
 constexpr int kMaxContext = 1 << 30;
@@ -151,7 +155,7 @@ template <int V> struct Shape {
     static constexpr int kOffClc = (kOffMax + 8 * V * 4 + 15) / 16 * 16;
     static constexpr int kOffBar = kOffClc + 16;
     static constexpr int kBars = 4 * kStages + 2 + 3 + 3 * kItems + 1;
-    static constexpr int kEnd = kOffBar + kBars * 8 + 16;
+    static constexpr int kEnd = kOffBar + kBars * 8 + 24;  // and tensor memory's address, flags, the hook's wait limit
     static constexpr int kReadEnd = kOffP + kN * kRowBytes;    // the last byte a product may read
     static constexpr int kSmemBytes = kEnd > kReadEnd ? kEnd : kReadEnd;
     // tensor memory: S in two buffers, O in one
@@ -324,7 +328,7 @@ __device__ __forceinline__ bool canceled(const void *answer, int &x, int &y, int
 
 // ------------------------------------------------------------------- kernel
 
-template <typename T, int D, int G>
+template <typename T, int D, int G, bool kHook = false>
 __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128 / D)>::kCtas)
     decode_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                   const DecodeParams p) {
@@ -360,6 +364,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
     volatile int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
     volatile int *loaded = reinterpret_cast<int *>(tmem_slot + 2);  // tiles that warp 5 has asked for
 
+    uint64_t *const wl = kHook ? bars + Sh::kBars + 2 : nullptr;  // (nullptr: the library's bound)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int bs_shift = p.bs_shift;
     const int blocks = kTok >> bs_shift;      // per tile: 4, 8 or 16
@@ -394,6 +399,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
         }
         *abort_flag = 0;
         *loaded = 0;
+        if constexpr (kHook) *wl = p.wait_limit_ns;
         fence_mbar_init();
         fence_proxy_async_smem();
     }
@@ -419,7 +425,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
             for (int n = 0; sound; ++n) {
                 const int slot = n % kItems;
                 if (n >= kItems) {
-                    sound = __all_sync(0xffffffffu, mbar_wait(i_empty + slot, (n / kItems - 1) & 1) && !*abort_flag);
+                    sound = __all_sync(0xffffffffu, mbar_wait(i_empty + slot, (n / kItems - 1) & 1, wl) && !*abort_flag);
                     if (!sound) break;
                 }
                 Item &it = items[slot];
@@ -543,7 +549,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                         const uint64_t t0 = global_ns();
                         for (uint32_t i = 1; sound && tiles - *loaded > kClaimAhead; ++i) {
                             __nanosleep(64);
-                            if (*abort_flag || ((i & 63u) == 0u && global_ns() - t0 > kWaitLimitNs * 4)) sound = false;
+                            if (*abort_flag || ((i & 63u) == 0u && global_ns() - t0 > 4 * (wl ? *wl : kWaitLimitNs))) sound = false;
                         }
                     }
                     sound = __all_sync(0xffffffffu, sound && !*abort_flag);
@@ -553,7 +559,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                         mbar_arrive_expect_tx(clc, 16);
                         try_cancel(sm + Sh::kOffClc, clc);
                     }
-                    sound = __all_sync(0xffffffffu, mbar_wait(clc, n & 1));
+                    sound = __all_sync(0xffffffffu, mbar_wait(clc, n & 1, wl));
                     if (sound) more = canceled(sm + Sh::kOffClc, x, y, z);
                     __syncwarp();
                 }
@@ -571,14 +577,14 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
             bool sound = true;
             for (int n = 0; sound; ++n) {
                 const int slot = n % kItems;
-                sound = __all_sync(0xffffffffu, mbar_wait(i_full + slot, (n / kItems) & 1) && !*abort_flag);
+                sound = __all_sync(0xffffffffu, mbar_wait(i_full + slot, (n / kItems) & 1, wl) && !*abort_flag);
                 if (!sound) break;
                 const Item &it = items[slot];
                 const int ntiles = it.ntiles;
                 if (ntiles < 0) break;
-                const int kvh = it.kvh, b0 = it.first >> bs_shift;
+                const int kvh = it.kvh, seq = it.s, b0 = it.first >> bs_shift;
                 const int nblk = (it.end + (1 << bs_shift) - 1) >> bs_shift;
-                const int32_t *trow = p.tables + (size_t)it.s * p.max_blocks;
+                const int32_t *trow = p.tables + (size_t)seq * p.max_blocks;
                 int id = lane < kMaxBlocks ? it.ids[lane] : -1;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(i_empty + slot);
@@ -595,16 +601,18 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                 for (int j = 0; j < ntiles; ++j, ++t) {
                     const int b = t % kStages;
                     if (t >= kStages) {
-                        sound = __all_sync(0xffffffffu, mbar_wait(empty + b, (t / kStages - 1) & 1) && !*abort_flag);
+                        sound = __all_sync(0xffffffffu, mbar_wait(empty + b, (t / kStages - 1) & 1, wl) && !*abort_flag);
                         if (!sound) break;
                     }
                     const bool here = lane < blocks && b0 + j * blocks + lane < nblk;
                     const bool ok = here && id >= 0 && id < p.num_blocks;
                     if (here && !ok && !is_v) record_error(p.err, PA_DEVERR_BLOCK_ID);
                     const unsigned m = __ballot_sync(0xffffffffu, ok);
-                    if (lane == 0) mbar_arrive_expect_tx(full + b, __popc(m) * rows * kRowBytes);
+                    const bool withheld = kHook && !is_v && seq == p.withhold_seq && kvh == p.withhold_kvh &&
+                                          j == p.withhold_tile;
+                    if (lane == 0 && !withheld) mbar_arrive_expect_tx(full + b, __popc(m) * rows * kRowBytes);
                     __syncwarp();
-                    if (ok)
+                    if (ok && !withheld)
                         load_once(ring + b * kTile + lane * rows * kRowBytes, map, (id * p.num_kv_heads + kvh) * rows,
                                   full + b, policy);
                     if (!is_v) {
@@ -628,7 +636,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
             }
             if (!sound && lane == 0) give_up();
             // copies in flight land before the CTA leaves
-            for (int i = max(0, t - kStages); i < t; ++i) mbar_wait(full + i % kStages, (i / kStages) & 1);
+            for (int i = max(0, t - kStages); i < t; ++i) mbar_wait(full + i % kStages, (i / kStages) & 1, wl);
             __syncwarp();
         } else {
             // ========================================================= MMA warp
@@ -644,7 +652,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                         // ended whose O is still to be issued here, so that goes first.
                         const int next = (n + 1) % kItems;
                         if (done == issued || mbar_test(q_full + next, ((n + 1) / kItems) & 1)) {
-                            sound = mbar_wait(q_full + next, ((n + 1) / kItems) & 1) && !*abort_flag;
+                            sound = mbar_wait(q_full + next, ((n + 1) / kItems) & 1, wl) && !*abort_flag;
                             if (!sound) break;
                             if (n >= 0) mbar_arrive(i_empty + slot);
                             ++n;
@@ -659,7 +667,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                     }
                     if (left > 0 && issued < done + 2) {
                         const int b = issued % kStages;
-                        sound = mbar_wait(k_full + b, (issued / kStages) & 1) && !*abort_flag;
+                        sound = mbar_wait(k_full + b, (issued / kStages) & 1, wl) && !*abort_flag;
                         if (!sound) break;
                         fence_after();
                         const uint32_t ka = base + Sh::kOffK + b * kTile, qa = base + Sh::kOffQ + slot * Sh::kDigits;
@@ -675,7 +683,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                     }
                     if (done == issued) break;  // no more items (with some, the next one was taken above)
                     const int b = done % kStages;
-                    sound = mbar_wait(p_full, done & 1) && mbar_wait(v_full + b, (done / kStages) & 1) && !*abort_flag;
+                    sound = mbar_wait(p_full, done & 1, wl) && mbar_wait(v_full + b, (done / kStages) & 1, wl) && !*abort_flag;
                     if (!sound) break;
                     fence_after();
                     const uint32_t va = base + Sh::kOffV + b * kTile, pa_ = base + Sh::kOffP;
@@ -689,7 +697,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                 if (!sound) give_up();
                 // tensor memory is freed below: every product issued must have finished
                 mma_commit(idle);
-                if (!mbar_wait(idle, 0)) record_error(p.err, PA_DEVERR_TIMEOUT);
+                if (!mbar_wait(idle, 0, wl)) record_error(p.err, PA_DEVERR_TIMEOUT);
             }
             __syncwarp();
         }
@@ -710,7 +718,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
         bool ok = true;
         for (int n = 0; ok; ++n) {
             const int slot = n % kItems;
-            bool sound = __all_sync(0xffffffffu, mbar_wait(q_full + slot, (n / kItems) & 1) && !*abort_flag);
+            bool sound = __all_sync(0xffffffffu, mbar_wait(q_full + slot, (n / kItems) & 1, wl) && !*abort_flag);
             ok = sync_and<kSoftmaxThreads>(sound);
             if (!ok) break;
             const Item &it = items[slot];
@@ -751,7 +759,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
             };
             for (int j = 0; j < ntiles; ++j, ++t) {
                 float *wm = wmax + (t & 1) * 4 * kV;
-                sound = __all_sync(0xffffffffu, sound && mbar_wait(s_full + (t & 1), (t >> 1) & 1) && !*abort_flag);
+                sound = __all_sync(0xffffffffu, sound && mbar_wait(s_full + (t & 1), (t >> 1) & 1, wl) && !*abort_flag);
                 float x[kSV];  // log2 of the weight
                 if (sound) {
                     fence_after();
@@ -824,7 +832,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
 #pragma unroll
                 for (int v = 0; v < kSV; ++v) mt[v] = fmaxf(mt[v], kNone);  // finite, though the weights all be 0
                 if (j > 0) {  // O of the tile before is there: P and O are free once it is added up
-                    sound = __all_sync(0xffffffffu, mbar_wait(o_full, (t - 1) & 1) && !*abort_flag);
+                    sound = __all_sync(0xffffffffu, mbar_wait(o_full, (t - 1) & 1, wl) && !*abort_flag);
                     if (!sound) continue;  // (the next barrier tells the others)
                     fence_after();
                     add_tile();
@@ -855,7 +863,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
             }
             if (!ok) break;
             if (ntiles > 0) {
-                sound = __all_sync(0xffffffffu, sound && mbar_wait(o_full, (t - 1) & 1) && !*abort_flag);
+                sound = __all_sync(0xffffffffu, sound && mbar_wait(o_full, (t - 1) & 1, wl) && !*abort_flag);
                 if (sound) {
                     fence_after();
                     add_tile();
@@ -995,10 +1003,10 @@ template <int D> __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(
     store_out(p.out, row * D + d, den != 0.f ? num / den : 0.f, p.out_dtype);
 }
 
-template <typename T, int D, int G>
+template <typename T, int D, int G, bool kHook = false>
 static cudaError_t launch_decode_t(const CUtensorMap &km, const CUtensorMap &vm, DecodeParams p, cudaStream_t stream) {
     using Sh = Shape<G * (128 / D)>;
-    auto kern = decode_kernel<T, D, G>;
+    auto kern = decode_kernel<T, D, G, kHook>;
     static AttrCache attr;
     static std::atomic<int> regs{0};
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), Sh::kSmemBytes, &attr);
@@ -1068,7 +1076,10 @@ extern "C" size_t pa_decode_q8b_workspace_bytes(int num_seqs, int num_heads, int
     return P ? pa_splitk_workspace_bytes(num_seqs, num_heads, head_dim, max_context_len, P) : 16;
 }
 
-extern "C" int pa_decode_q8b(void *out, const void *query, pa_dtype q_dtype, const int8_t *k_cache,
+namespace {
+
+// pa_decode_q8b; hook.withhold_tile >= 0: its test form.
+int decode_q8b_call(const q8b::DecodeParams &hook, void *out, const void *query, pa_dtype q_dtype, const int8_t *k_cache,
                              const int8_t *v_cache, const float *k_scale, const float *v_scale,
                              const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
                              int num_seqs, int num_heads, int num_kv_heads, int head_dim, float scale, int block_size,
@@ -1099,7 +1110,7 @@ extern "C" int pa_decode_q8b(void *out, const void *query, pa_dtype q_dtype, con
         !aligned_to(k_scale, 16) || !aligned_to(v_scale, 16) || !aligned_to(workspace, 16) ||
         !aligned_to(block_tables, 4) || !aligned_to(context_lens, 4) || !aligned_to(seq_order, 4))
         return PA_ERR_ALIGN;
-    q8b::DecodeParams p{};
+    q8b::DecodeParams p = hook;
     if (device_error_word(&p.err) != cudaSuccess) return PA_ERR_CUDA;
     p.out = out;
     p.query = query;
@@ -1137,8 +1148,11 @@ extern "C" int pa_decode_q8b(void *out, const void *query, pa_dtype q_dtype, con
         !encode_rows_2d(&vm, CU_TENSOR_MAP_DATA_TYPE_UINT8, v_cache, 128, rows ? rows : 1, 128, 128, box,
                         CU_TENSOR_MAP_SWIZZLE_128B))
         return PA_ERR_CUDA;
-    cudaError_t e = q_dtype == PA_F16 ? q8b::launch_decode<__half>(km, vm, p, head_dim, stream)
-                                      : q8b::launch_decode<__nv_bfloat16>(km, vm, p, head_dim, stream);
+    cudaError_t e;
+    if (hook.withhold_tile >= 0) e = q8b::launch_decode_t<__half, 128, 1, true>(km, vm, p, stream);
+    else
+        e = q_dtype == PA_F16 ? q8b::launch_decode<__half>(km, vm, p, head_dim, stream)
+                              : q8b::launch_decode<__nv_bfloat16>(km, vm, p, head_dim, stream);
     if (e == cudaSuccess && P) {
         const dim3 grid((unsigned)num_heads, (unsigned)num_seqs);
         const unsigned block = q8b::kJoinWarps * 32;
@@ -1146,4 +1160,43 @@ extern "C" int pa_decode_q8b(void *out, const void *query, pa_dtype q_dtype, con
                             : launch_after(q8b::join_kernel<64>, grid, block, 0, 1, stream, p);
     }
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" int pa_decode_q8b(void *out, const void *query, pa_dtype q_dtype, const int8_t *k_cache,
+                             const int8_t *v_cache, const float *k_scale, const float *v_scale,
+                             const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                             int num_seqs, int num_heads, int num_kv_heads, int head_dim, float scale, int block_size,
+                             int num_blocks, int max_context_len, pa_dtype out_dtype, const int32_t *seq_order,
+                             void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    q8b::DecodeParams none{};
+    none.withhold_tile = -1;
+    return decode_q8b_call(none, out, query, q_dtype, k_cache, v_cache, k_scale, v_scale, block_tables,
+                           max_blocks_per_seq, context_lens, num_seqs, num_heads, num_kv_heads, head_dim, scale,
+                           block_size, num_blocks, max_context_len, out_dtype, seq_order, workspace, workspace_bytes,
+                           stream);
+}
+
+extern "C" int pa_decode_q8b_withhold_tile(void *out, const void *query, pa_dtype q_dtype, const int8_t *k_cache,
+                                           const int8_t *v_cache, const float *k_scale, const float *v_scale,
+                                           const int32_t *block_tables, int max_blocks_per_seq,
+                                           const int32_t *context_lens, int num_seqs, int num_heads, int num_kv_heads,
+                                           int head_dim, float scale, int block_size, int num_blocks,
+                                           int max_context_len, pa_dtype out_dtype, int seq, int kv_head, int tile,
+                                           unsigned long long wait_limit_ns, cudaStream_t stream) {
+    if (q_dtype != PA_F16) return PA_ERR_DTYPE;  // the hook's instance
+    if (head_dim != 128) return PA_ERR_HEAD_DIM;
+    if (num_heads != num_kv_heads) return PA_ERR_HEADS;
+    if (seq < 0 || seq >= num_seqs || kv_head < 0 || kv_head >= num_kv_heads || tile < 0 || wait_limit_ns < 100000ull ||
+        wait_limit_ns > 1000000000ull)
+        return PA_ERR_SHAPE;
+    q8b::DecodeParams hook{};
+    hook.withhold_seq = seq;
+    hook.withhold_kvh = kv_head;
+    hook.withhold_tile = tile;
+    hook.wait_limit_ns = wait_limit_ns;
+    return decode_q8b_call(hook, out, query, q_dtype, k_cache, v_cache, k_scale, v_scale, block_tables,
+                           max_blocks_per_seq, context_lens, num_seqs, num_heads, num_kv_heads, head_dim, scale,
+                           block_size, num_blocks, max_context_len, out_dtype, nullptr, nullptr, 0, stream);
 }

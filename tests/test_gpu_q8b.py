@@ -458,6 +458,28 @@ def test_decode_non_finite_query_gives_nan_rows_only_there(pa, D):
         assert (out[1] == 0).all()
 
 
+@pytest.mark.parametrize("tile", [0, 1, 3])
+def test_decode_wait_that_runs_out_returns_and_reports(pa, tile):
+    """One K tile's copy never issued: the launch ends, the error word says
+    so, every other output is right, and the next call is sound."""
+    c = Case(3, 3, 128, 16, [500, 40, 700], seed=41)
+    args = [c.q.half().cuda(), *[torch.from_numpy(a).cuda() for a in (c.kq, c.vq, c.ks, c.vs, c.tables, c.ctx)], c.scale, 700]
+    want = torch.empty((3, 3, 128), device="cuda")
+    pa.pa_decode_q8b(want, *args)
+    out = torch.empty_like(want)
+    pa.pa_decode_q8b_withhold_tile(out, *args, 0, 1, tile, 20_000_000)
+    torch.cuda.synchronize()
+    assert pa.pa_read_device_errors() == 0x8
+    others = torch.ones((3, 3), dtype=torch.bool, device="cuda")
+    others[0, 1] = False
+    assert torch.equal(out[others], want[others])
+    again = torch.empty_like(want)
+    pa.pa_decode_q8b(again, *args)
+    pa.pa_decode_q8b_withhold_tile(out, *args, 1, 2, 5, 20_000_000)  # past that sequence's end: nothing withheld
+    assert pa.pa_read_device_errors() == 0
+    assert torch.equal(again, want) and torch.equal(out, want)
+
+
 def test_decode_empty_batches(pa):
     c = Case(4, 2, 128, 16, [0, 0], seed=37)
     assert (c.run(pa, torch.float16) == 0).all()

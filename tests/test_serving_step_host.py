@@ -67,6 +67,17 @@ def test_decode_q8b_host_checks(pa, kw, code):
     assert pa._lib.pa_decode_q8b(*a.values(), None) == code
 
 
+@pytest.mark.parametrize("kw,code", [
+    (dict(q_dt=2, out_dt=2), -2), (dict(D=64), -5), (dict(Hq=4), -4), (dict(seq=2), -3), (dict(seq=-1), -3), (dict(head=2), -3),
+    (dict(tile=-1), -3), (dict(limit=99_999), -3), (dict(limit=1_000_000_001), -3), (dict(kc=None), -1), (dict(out=A + 8), -7),
+])
+def test_decode_q8b_withhold_tile_host_checks(pa, kw, code):
+    a = dict(out=A, q=A, q_dt=1, kc=A, vc=A, ks=A, vs=A, tables=A, mb=4096, ctx=A, S=2, Hq=2, Hkv=2, D=128, scale=0.1,
+             bs=16, nb=40, L=60000, out_dt=1, seq=1, head=1, tile=0, limit=1_000_000)
+    a.update(kw)
+    assert pa._lib.pa_decode_q8b_withhold_tile(*a.values(), None) == code
+
+
 def test_decode_q8b_workspace_bytes(pa):
     f = pa.pa_decode_q8b_workspace_bytes
     assert f(-1, 8, 2, 128, 100) == 0 and f(1, 0, 2, 128, 100) == 0 and f(1, 8, 2, 128, -1) == 0
