@@ -94,9 +94,9 @@ constexpr int kG = 8;                          // query heads per item, at most
 constexpr int kRowBytes = 128;
 constexpr int kTile = 128 * kRowBytes;         // 16 KB of K or V
 constexpr int kClaimAhead = 4;                 // tiles still to be loaded when another item is claimed
-// Splitting along the tokens, in tiles: 16-tile pieces measured best of 8, 12,
-// 16, 32 and 64 for 8 sequences of 32,768 to 131,072 tokens (163, 161, 158, 172, 195 us).
-constexpr int kPiece = 16, kPieceMost = 48;
+// Splitting along the tokens: pieces of at most 16 tiles, which measured best of 8,
+// 12, 16, 32 and 64 for 8 sequences of 32,768 to 131,072 tokens (163, 161, 158, 172, 195 us).
+constexpr int kPiece = 16;
 constexpr int kMaxBlocks = 16;                 // blocks of a tile, at most
 // Virtual heads from which the softmax has two warpgroups: 16 (222 sequences of
 // 4096 tokens, 8 kv heads of 64 with 8 query heads each: 273 -> 227 us); at 8 the
@@ -117,7 +117,7 @@ struct Item {
     int first;    // its tokens: first .. end - 1
     int end;
     int part;
-    int write;    // whether it has an output (else it is skipped)
+    int pad;
     int ids[kMaxBlocks];  // blocks of the first tile (-1: none)
 };
 
@@ -422,15 +422,18 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
             int x = blockIdx.x, y = blockIdx.y, z = blockIdx.z;
             bool more = true, sound = true;
             int tiles = 0;  // of all items so far
-            for (int n = 0; sound; ++n) {
+            // n: items handed on (a partition past its sequence's end is dropped here), claims: answers asked for
+            for (int n = 0, claims = 0; sound;) {
                 const int slot = n % kItems;
-                if (n >= kItems) {
-                    sound = __all_sync(0xffffffffu, mbar_wait(i_empty + slot, (n / kItems - 1) & 1, wl) && !*abort_flag);
-                    if (!sound) break;
-                }
                 Item &it = items[slot];
+                auto slot_free = [&]() {
+                    if (n >= kItems)
+                        sound = __all_sync(0xffffffffu, mbar_wait(i_empty + slot, (n / kItems - 1) & 1, wl) && !*abort_flag);
+                    return sound;
+                };
                 if (!more) {
                     allow_next();
+                    if (!slot_free()) break;
                     if (lane == 0) {
                         it.ntiles = -1;
                         mbar_arrive(i_full + slot);
@@ -439,13 +442,14 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                     break;
                 }
                 // ---- the item
-                int s = z, write = 1;
+                int s = z;
+                bool real = true;  // whether it has an output (else it is dropped)
                 if (p.seq_order) {
                     s = __ldg(p.seq_order + z);
                     if (s < 0 || s >= p.num_seqs) {
                         if (lane == 0) record_error(p.err, PA_DEVERR_CONTEXT);
                         s = 0;
-                        write = 0;
+                        real = false;
                     }
                 }
                 const int kvh = y / p.sub_groups, sub = y % p.sub_groups;
@@ -466,81 +470,84 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                 int id = lane < blocks && lb < p.max_blocks ? __ldg(p.tables + (size_t)s * p.max_blocks + lb) : -1;
                 int L = __ldg(p.ctx + s);
                 const int room = (int)min((long long)p.max_blocks << bs_shift, (long long)p.max_ctx);
-                if (write && (L < 0 || L > room)) {
+                if (real && (L < 0 || L > room)) {
                     if (lane == 0) record_error(p.err, PA_DEVERR_CONTEXT);
                     L = L < 0 ? 0 : room;
                 }
                 if (p.partition_size) {
                     L = min(L, first + p.partition_size);
-                    if (first >= L) write = 0;  // no such partition: its entry is not read
+                    if (first >= L) real = false;  // no such partition: its entry is not read
                 }
-                if (!write) L = first;
+                if (!real) L = first;
                 const int ntiles = L > first ? (L - first + kTok - 1) / kTok : 0;
                 if (lb >= (L + (1 << bs_shift) - 1) >> bs_shift) id = -1;
-                if (lane < kMaxBlocks) it.ids[lane] = id;
-                if (lane == 0) {
-                    it.ntiles = ntiles;
-                    it.s = s;
-                    it.head0 = head0;
-                    it.kvh = kvh;
-                    it.first = first;
-                    it.end = L;
-                    it.part = x;
-                    it.write = write;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(i_full + slot);  // the load warps can start
-                // ---- the query's digits
-                unsigned char *Qs = sm + Sh::kOffQ + slot * Sh::kDigits;
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const T *raw_g = reinterpret_cast<const T *>(&raw[g]);
-                    float q[kE];
-                    uint32_t mag = 0;  // the largest |q|, as bits (they order like the values, infinities and NaN on top)
-#pragma unroll
-                    for (int e = 0; e < kE; ++e) {
-                        q[e] = (float)raw_g[e];
-                        mag = max(mag, __float_as_uint(q[e]) & 0x7fffffffu);
+                if (real) {
+                    if (!slot_free()) break;
+                    if (lane < kMaxBlocks) it.ids[lane] = id;
+                    if (lane == 0) {
+                        it.ntiles = ntiles;
+                        it.s = s;
+                        it.head0 = head0;
+                        it.kvh = kvh;
+                        it.first = first;
+                        it.end = L;
+                        it.part = x;
                     }
-                    mag = __reduce_max_sync(0xffffffffu, mag);
-                    const float amax = __uint_as_float(mag);
-                    const bool finite = mag < 0x7f800000u;
-                    // a query below 2^-100 counts as zero (its unit's reciprocal would not be finite)
-                    const bool live = finite && amax >= 7.888609e-31f;
-                    const float inv = live ? kQUnit / amax : 0.f;
-                    uint32_t w[3] = {0u, 0u, 0u};  // the lane's kE digits of each place
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(i_full + slot);  // the load warps can start
+                    // ---- the query's digits
+                    unsigned char *Qs = sm + Sh::kOffQ + slot * Sh::kDigits;
 #pragma unroll
-                    for (int e = 0; e < kE; ++e) {
-                        // (the product may round up past the unit)
-                        const int v = live ? max(-kQMax, min(kQMax, __float2int_rn(q[e] * inv))) : 0;
-                        const int c = (int)(int8_t)v, v1 = (v - c) >> 8;
-                        const int b = (int)(int8_t)v1, a = (v1 - b) >> 8;
-                        w[0] |= (uint32_t)(a & 0xff) << (8 * e);
-                        w[1] |= (uint32_t)(b & 0xff) << (8 * e);
-                        w[2] |= (uint32_t)(c & 0xff) << (8 * e);
-                    }
+                    for (int g = 0; g < G; ++g) {
+                        const T *raw_g = reinterpret_cast<const T *>(&raw[g]);
+                        float q[kE];
+                        uint32_t mag = 0;  // the largest |q|, as bits (they order like the values, infinities and NaN on top)
 #pragma unroll
-                    for (int par = 0; par < kPar; ++par)
-#pragma unroll
-                        for (int i = 0; i < 3; ++i) {
-                            const int r = (par * G + g) * 3 + i;  // digit row; its 16-byte chunks are swizzled
-                            auto at = [&](int half) {
-                                return Qs + r * kRowBytes + ((half * D + lane * kE) ^ ((r & 7) << 4));
-                            };
-                            if constexpr (kPar == 1) {
-                                *reinterpret_cast<uint32_t *>(at(0)) = w[i];
-                            } else {
-                                *reinterpret_cast<uint16_t *>(at(par)) = (uint16_t)w[i];
-                                *reinterpret_cast<uint16_t *>(at(1 - par)) = 0;
-                            }
+                        for (int e = 0; e < kE; ++e) {
+                            q[e] = (float)raw_g[e];
+                            mag = max(mag, __float_as_uint(q[e]) & 0x7fffffffu);
                         }
-                    // (a query that is not finite makes its scores, and so its row, NaN)
-                    if (lane < kPar)
-                        qscale[slot * kV + lane * G + g] = live ? amax / kQUnit * p.scale_log2 : finite ? 0.f : NAN;
+                        mag = __reduce_max_sync(0xffffffffu, mag);
+                        const float amax = __uint_as_float(mag);
+                        const bool finite = mag < 0x7f800000u;
+                        // a query below 2^-100 counts as zero (its unit's reciprocal would not be finite)
+                        const bool live = finite && amax >= 7.888609e-31f;
+                        const float inv = live ? kQUnit / amax : 0.f;
+                        uint32_t w[3] = {0u, 0u, 0u};  // the lane's kE digits of each place
+#pragma unroll
+                        for (int e = 0; e < kE; ++e) {
+                            // (the product may round up past the unit)
+                            const int v = live ? max(-kQMax, min(kQMax, __float2int_rn(q[e] * inv))) : 0;
+                            const int c = (int)(int8_t)v, v1 = (v - c) >> 8;
+                            const int b = (int)(int8_t)v1, a = (v1 - b) >> 8;
+                            w[0] |= (uint32_t)(a & 0xff) << (8 * e);
+                            w[1] |= (uint32_t)(b & 0xff) << (8 * e);
+                            w[2] |= (uint32_t)(c & 0xff) << (8 * e);
+                        }
+#pragma unroll
+                        for (int par = 0; par < kPar; ++par)
+#pragma unroll
+                            for (int i = 0; i < 3; ++i) {
+                                const int r = (par * G + g) * 3 + i;  // digit row; its 16-byte chunks are swizzled
+                                auto at = [&](int half) {
+                                    return Qs + r * kRowBytes + ((half * D + lane * kE) ^ ((r & 7) << 4));
+                                };
+                                if constexpr (kPar == 1) {
+                                    *reinterpret_cast<uint32_t *>(at(0)) = w[i];
+                                } else {
+                                    *reinterpret_cast<uint16_t *>(at(par)) = (uint16_t)w[i];
+                                    *reinterpret_cast<uint16_t *>(at(1 - par)) = 0;
+                                }
+                            }
+                        // (a query that is not finite makes its scores, and so its row, NaN)
+                        if (lane < kPar)
+                            qscale[slot * kV + lane * G + g] = live ? amax / kQUnit * p.scale_log2 : finite ? 0.f : NAN;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(q_full + slot);
+                    ++n;
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_full + slot);
                 // ---- the next one, once few tiles are left to load
                 tiles += ntiles;
                 more = false;
@@ -559,7 +566,8 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                         mbar_arrive_expect_tx(clc, 16);
                         try_cancel(sm + Sh::kOffClc, clc);
                     }
-                    sound = __all_sync(0xffffffffu, mbar_wait(clc, n & 1, wl));
+                    sound = __all_sync(0xffffffffu, mbar_wait(clc, claims & 1, wl));
+                    ++claims;
                     if (sound) more = canceled(sm + Sh::kOffClc, x, y, z);
                     __syncwarp();
                 }
@@ -724,7 +732,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
             const Item &it = items[slot];
             const int ntiles = it.ntiles;
             if (ntiles < 0) break;
-            const int L = it.end, first = it.first, part = it.part, write = it.write;
+            const int L = it.end, first = it.first, part = it.part;
             const size_t row0 = (size_t)it.s * p.num_heads + it.head0;  // output row of head 0
             const int g_valid = min(G, p.group - it.head0 % p.group / kG * kG);
             float qs[kSV];
@@ -900,7 +908,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                 if (kPar == 2 && r >= D) red_o[(g0 + g) * D + r - D] = o[g];
             }
             if constexpr (kPar == 2) named_bar_sync(1, kSoftmaxThreads);
-            if (r < D && write) {
+            if (r < D) {
 #pragma unroll
                 for (int g = 0; g < kOG; ++g) {
                     if (g0 + g >= g_valid) continue;
@@ -934,10 +942,11 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
 // Joins the partitions: out = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) l_p.
 // One CTA per (head, sequence); warp w takes partitions w, w + kJoinWarps, ..,
 // a lane D / 32 dims, and the warps are joined in shared memory. A batch of
-// kJoinWarps * kU partitions costs one trip to L2, which is all that bounds it.
-constexpr int kJoinWarps = 16;
-
-template <int D> __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const DecodeParams p) {
+// kJoinWarps * kU partitions costs one trip to L2, which is all that bounds it:
+// 16 warps for many partitions; 4 for up to 16 of them, where a batch's CTAs
+// then fit the GPU at once (40 sequences of 8 heads: 25.2 us with 16 warps,
+// decode included, 24.4 with 4).
+template <int D, int kJoinWarps> __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const DecodeParams p) {
     constexpr int kE = D / 32, kU = 4;
     using Vec = std::conditional_t<kE == 4, float4, float2>;
     __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps], sm_o[kJoinWarps][D];
@@ -1036,10 +1045,10 @@ static cudaError_t launch_decode(const CUtensorMap &km, const CUtensorMap &vm, c
 #undef PA_Q8B
 }
 
-// Tokens of a partition (0: none). One item per resident CTA, as far as the
-// longest context tells, where that leaves a CTA at most kPieceMost tiles; longer
-// work goes in pieces of about kPiece tiles, which the CTAs take one after
-// another, so that ragged lengths even out.
+// Tokens of a partition (0: none). One piece per resident CTA, as far as the
+// longest context tells (two or three pieces measured 0 to 30 % slower for 1 to 40
+// sequences); longer work goes in pieces of kPiece tiles, which the CTAs take one
+// after another, so that ragged lengths even out.
 static int partition_of(int num_seqs, int rows_y, int group, int head_dim, int max_ctx) {
     const int tok = 128 * (128 / head_dim);
     const long long items = (long long)num_seqs * rows_y, tiles = ((long long)max_ctx + tok - 1) / tok;
@@ -1047,7 +1056,7 @@ static int partition_of(int num_seqs, int rows_y, int group, int head_dim, int m
     const long long ctas = (heads >= kTwoTeams ? 2ll : 3ll) * sm_count();
     if (items >= ctas || tiles < 2) return 0;
     long long per = (items * tiles + ctas - 1) / ctas;
-    if (per > kPieceMost) per = kPiece;
+    if (per > kPiece) per = kPiece;
     return per >= tiles ? 0 : (int)(per * tok);
 }
 
@@ -1155,9 +1164,10 @@ int decode_q8b_call(const q8b::DecodeParams &hook, void *out, const void *query,
                               : q8b::launch_decode<__nv_bfloat16>(km, vm, p, head_dim, stream);
     if (e == cudaSuccess && P) {
         const dim3 grid((unsigned)num_heads, (unsigned)num_seqs);
-        const unsigned block = q8b::kJoinWarps * 32;
-        e = head_dim == 128 ? launch_after(q8b::join_kernel<128>, grid, block, 0, 1, stream, p)
-                            : launch_after(q8b::join_kernel<64>, grid, block, 0, 1, stream, p);
+        const bool few = p.max_parts <= 16;  // a batch of 4 warps
+        auto join = head_dim == 128 ? (few ? q8b::join_kernel<128, 4> : q8b::join_kernel<128, 16>)
+                                    : (few ? q8b::join_kernel<64, 4> : q8b::join_kernel<64, 16>);
+        e = launch_after(join, grid, few ? 128u : 512u, 0, 1, stream, p);
     }
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
