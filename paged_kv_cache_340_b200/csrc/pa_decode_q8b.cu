@@ -13,7 +13,7 @@
 //   * q_d = qs * (65536 a + 256 b + c), signed digits, qs = max|q| / 8355711:
 //     23 bits of the head's largest element;
 //   * w_t = p_t v_scale_t / (the tile's largest one) = (65536 a + 256 b + c) /
-//     16777215, unsigned digits: 24 bits of the tile's largest weight. The
+//     8388607, unsigned digits: 23 bits of the tile's largest weight. The
 //     block scales are folded in here, and the tile's largest weight is the
 //     unit, so a tile's sum is exact to 2^-17 of itself whatever the others
 //     hold; tiles are joined in fp32.
@@ -104,7 +104,7 @@ constexpr int kMaxBlocks = 16;                 // blocks of a tile, at most
 constexpr int kTwoTeams = 16;
 constexpr int kQMax = 8355711;                 // 127 * 65536 + 127 * 256 + 127, three signed digits
 constexpr float kQUnit = 8355711.f;
-constexpr float kWUnit = 16777215.f;           // 2^24 - 1
+constexpr float kWUnit = 8388607.f;            // 2^23 - 1
 constexpr float kNone = -3e38f;                // below every score: the maximum of no tokens
 constexpr float kRaise = 16.f;                 // see the softmax
 
@@ -856,7 +856,8 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                 // ---- the weights' digits, row 3 v + i, byte r of the row (its 16-byte chunks swizzled)
 #pragma unroll
                 for (int v = 0; v < kSV; ++v) {
-                    const unsigned u = __float2uint_rn(fast_exp2(x[v] - mt[v]) * kWUnit);
+                    // the whole number is the sum's mantissa: no conversion (bit 23 is 0 in its exponent)
+                    const unsigned u = __float_as_uint(fmaf(fast_exp2(x[v] - mt[v]), kWUnit, 8388608.f));
                     const int d = 3 * v, d0 = 3 * v0;  // (3 v0 is a multiple of 8 with two teams, else 0)
                     static_assert(kTeams == 1 || 3 * kSV % 8 == 0 || kSV == 4, "swizzle phase");
                     const int ph = kTeams == 1 || 3 * kSV % 8 == 0 ? 0 : d0 & 7;

@@ -10,7 +10,7 @@ sees. A score is a sum of D products held in at least 23 bits of its largest
 part, computed within 2^-20 of A = scale * log2(e) * sum_d |q_d k_d|, and
 exp2's own error is below 2^-20: every weight is off by at most
 ln2 * A * 2^-20 + 2^-20, relative. A weighted mean moves by at most twice the
-largest relative error of its weights times M. Weights held in 24 bits of a
+largest relative error of its weights times M. Weights held in 23 bits of a
 tile's largest one, 128 to a tile, lose another 2^-17 M; fp32 sums over L
 terms, a few 2^-24 sqrt(L). So
   |out - ref| <= M * (2 * (A + 1) * 2^-20 + 2^-17 + 2^-24 * sqrt(L) * 8)
