@@ -10,8 +10,8 @@
 //   O^T = V^T P^T (M 128 = head dims, N = probability columns, K = 128 tokens)
 // as tcgen05.mma kind::i8 with exact int32 sums. Query and probabilities enter
 // as fixed point in base 256, three columns a head:
-//   * q_d = qs * (65536 a + 256 b + c), signed digits, qs = max|q| / 8355711:
-//     23 bits of the head's largest element;
+//   * q_d = qs * (65536 a + 256 b + c), signed digits, qs = 2^-21 of the power of
+//     two of max|q|: elements down to 2^-11 (fp16) or 2^-14 (bf16) of it are exact;
 //   * w_t = p_t v_scale_t / (the tile's largest one) = (65536 a + 256 b + c) /
 //     8388607, unsigned digits: 23 bits of the tile's largest weight. The
 //     block scales are folded in here, and the tile's largest weight is the
@@ -102,8 +102,6 @@ constexpr int kMaxBlocks = 16;                 // blocks of a tile, at most
 // 4096 tokens, 8 kv heads of 64 with 8 query heads each: 273 -> 227 us); at 8 the
 // third CTA that one warpgroup leaves room for is worth more (151 against 167 us).
 constexpr int kTwoTeams = 16;
-constexpr int kQMax = 8355711;                 // 127 * 65536 + 127 * 256 + 127, three signed digits
-constexpr float kQUnit = 8355711.f;
 constexpr float kWUnit = 8388607.f;            // 2^23 - 1
 constexpr float kNone = -3e38f;                // below every score: the maximum of no tokens
 constexpr float kRaise = 16.f;                 // see the softmax
@@ -431,6 +429,15 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                         sound = __all_sync(0xffffffffu, mbar_wait(i_empty + slot, (n / kItems - 1) & 1, wl) && !*abort_flag);
                     return sound;
                 };
+                bool asked = false;
+                auto claim = [&]() {  // asks for the next item
+                    if (lane == 0) {
+                        fence_proxy_async_smem();  // the last answer has been read
+                        mbar_arrive_expect_tx(clc, 16);
+                        try_cancel(sm + Sh::kOffClc, clc);
+                    }
+                    asked = true;
+                };
                 if (!more) {
                     allow_next();
                     if (!slot_free()) break;
@@ -495,35 +502,44 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(i_full + slot);  // the load warps can start
+                    tiles += ntiles;
+                    if (p.steal && __all_sync(0xffffffffu, tiles - *loaded <= kClaimAhead)) claim();
                     // ---- the query's digits
                     unsigned char *Qs = sm + Sh::kOffQ + slot * Sh::kDigits;
+                    uint32_t mag[G];  // the largest |q|, as its bits (they order like the values, infinities and NaN on top)
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        const uint32_t *w = reinterpret_cast<const uint32_t *>(&raw[g]);
+                        uint32_t m = w[0] & 0x7fff7fffu;
+                        if constexpr (kE == 4) m = __vmaxu2(m, w[1] & 0x7fff7fffu);
+                        mag[g] = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xffffu));
+                    }
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
                         const T *raw_g = reinterpret_cast<const T *>(&raw[g]);
-                        float q[kE];
-                        uint32_t mag = 0;  // the largest |q|, as bits (they order like the values, infinities and NaN on top)
-#pragma unroll
-                        for (int e = 0; e < kE; ++e) {
-                            q[e] = (float)raw_g[e];
-                            mag = max(mag, __float_as_uint(q[e]) & 0x7fffffffu);
-                        }
-                        mag = __reduce_max_sync(0xffffffffu, mag);
-                        const float amax = __uint_as_float(mag);
-                        const bool finite = mag < 0x7f800000u;
+                        const unsigned short bits = (unsigned short)mag[g];
+                        const uint32_t e = __float_as_uint((float)*reinterpret_cast<const T *>(&bits)) >> 23;  // its exponent
+                        const bool finite = e < 255u;
                         // a query below 2^-100 counts as zero (its unit's reciprocal would not be finite)
-                        const bool live = finite && amax >= 7.888609e-31f;
-                        const float inv = live ? kQUnit / amax : 0.f;
-                        uint32_t w[3] = {0u, 0u, 0u};  // the lane's kE digits of each place
+                        const bool live = finite && e >= 27u;
+                        const float inv = live ? __uint_as_float((275u - e) << 23) : 0.f;
+                        uint32_t u[kE];  // the digits, plus 128 each
 #pragma unroll
-                        for (int e = 0; e < kE; ++e) {
-                            // (the product may round up past the unit)
-                            const int v = live ? max(-kQMax, min(kQMax, __float2int_rn(q[e] * inv))) : 0;
-                            const int c = (int)(int8_t)v, v1 = (v - c) >> 8;
-                            const int b = (int)(int8_t)v1, a = (v1 - b) >> 8;
-                            w[0] |= (uint32_t)(a & 0xff) << (8 * e);
-                            w[1] |= (uint32_t)(b & 0xff) << (8 * e);
-                            w[2] |= (uint32_t)(c & 0xff) << (8 * e);
+                        for (int i = 0; i < kE; ++i)
+                            u[i] = __float_as_uint(fmaf((float)raw_g[i], inv, 12582912.f)) + 0x408080u;
+                        uint32_t w[3];  // the lane's kE digits of each place
+                        if constexpr (kE == 4) {
+                            const uint32_t lo01 = __byte_perm(u[0], u[1], 0x5140), lo23 = __byte_perm(u[2], u[3], 0x5140);
+                            w[0] = __byte_perm(__byte_perm(u[0], u[1], 0x0062), __byte_perm(u[2], u[3], 0x0062), 0x5410);
+                            w[1] = __byte_perm(lo01, lo23, 0x7632);
+                            w[2] = __byte_perm(lo01, lo23, 0x5410);
+                        } else {
+                            w[0] = __byte_perm(u[0], u[1], 0x0062);
+                            w[1] = __byte_perm(u[0], u[1], 0x0051);
+                            w[2] = __byte_perm(u[0], u[1], 0x0040);
                         }
+#pragma unroll
+                        for (int i = 0; i < 3; ++i) w[i] ^= 0x80808080u;
 #pragma unroll
                         for (int par = 0; par < kPar; ++par)
 #pragma unroll
@@ -541,7 +557,8 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                             }
                         // (a query that is not finite makes its scores, and so its row, NaN)
                         if (lane < kPar)
-                            qscale[slot * kV + lane * G + g] = live ? amax / kQUnit * p.scale_log2 : finite ? 0.f : NAN;
+                            qscale[slot * kV + lane * G + g] = live ? __uint_as_float((e - 21u) << 23) * p.scale_log2
+                                                                    : finite ? 0.f : NAN;
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -549,10 +566,9 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                     ++n;
                 }
                 // ---- the next one, once few tiles are left to load
-                tiles += ntiles;
                 more = false;
                 if (p.steal) {
-                    if (tiles - *loaded > kClaimAhead) {
+                    if (!asked && tiles - *loaded > kClaimAhead) {
                         const uint64_t t0 = global_ns();
                         for (uint32_t i = 1; sound && tiles - *loaded > kClaimAhead; ++i) {
                             __nanosleep(64);
@@ -561,11 +577,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                     }
                     sound = __all_sync(0xffffffffu, sound && !*abort_flag);
                     if (!sound) break;
-                    if (lane == 0) {
-                        fence_proxy_async_smem();  // the last answer has been read
-                        mbar_arrive_expect_tx(clc, 16);
-                        try_cancel(sm + Sh::kOffClc, clc);
-                    }
+                    if (!asked) claim();
                     sound = __all_sync(0xffffffffu, mbar_wait(clc, claims & 1, wl));
                     ++claims;
                     if (sound) more = canceled(sm + Sh::kOffClc, x, y, z);
@@ -673,8 +685,25 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                             continue;
                         }
                     }
-                    if (left > 0 && issued < done + 2) {
-                        const int b = issued % kStages;
+                    // S or O, whichever has its operands first
+                    bool take_s = left > 0 && issued < done + 2, take_o = done < issued;
+                    if (!take_s && !take_o) break;  // no more items (with some, the next one was taken above)
+                    const int bs = issued % kStages, bo = done % kStages;
+                    if (take_s && take_o) {
+                        const uint64_t t0 = global_ns();
+                        for (uint32_t i = 1;; ++i) {
+                            take_s = mbar_test(k_full + bs, (issued / kStages) & 1);
+                            take_o = !take_s && mbar_test(p_full, done & 1) && mbar_test(v_full + bo, (done / kStages) & 1);
+                            if (take_s || take_o) break;
+                            if ((i & 63u) == 0u && (*abort_flag || global_ns() - t0 > (wl ? *wl : kWaitLimitNs))) {
+                                sound = false;
+                                break;
+                            }
+                        }
+                        if (!sound) break;
+                    }
+                    if (take_s) {
+                        const int b = bs;
                         sound = mbar_wait(k_full + b, (issued / kStages) & 1, wl) && !*abort_flag;
                         if (!sound) break;
                         fence_after();
@@ -689,8 +718,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                         --left;
                         continue;
                     }
-                    if (done == issued) break;  // no more items (with some, the next one was taken above)
-                    const int b = done % kStages;
+                    const int b = bo;
                     sound = mbar_wait(p_full, done & 1, wl) && mbar_wait(v_full + b, (done / kStages) & 1, wl) && !*abort_flag;
                     if (!sound) break;
                     fence_after();
@@ -892,41 +920,34 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
             warp_sums<kSV, 16>(l, lane);  // lane c * 32 / kSV holds head c's
             if (lane % (32 / kSV) == 0) red_l[quarter * kV + v0 + lane / (32 / kSV)] = l[0];
             named_bar_sync(1, kSoftmaxThreads);
-            float m[kOG], sum[kOG];
+            // lane g * kEnt + i: entry i of head g (its four quarters, twice at head_dim 64)
+            constexpr int kEnt = 4 * kPar;
+            const int hg = min(lane / kEnt, kOG - 1), ent = lane % kEnt;
+            const int at = (ent & 3) * kV + (ent >> 2) * G + g0 + hg;
+            const float mi = red_m[at];
+            float m = mi;
+#pragma unroll
+            for (int i = kEnt / 2; i; i /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+            float sum = red_l[at] * fast_exp2(mi - m);  // (a NaN query's sum is NaN)
+#pragma unroll
+            for (int i = kEnt / 2; i; i /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+            const float unit = p.partition_size ? 1.f / kWUnit : sum != 0.f ? 1.f / (sum * kWUnit) : 0.f;
 #pragma unroll
             for (int g = 0; g < kOG; ++g) {
-                const float *gm = red_m + g0 + g, *gl = red_l + g0 + g;  // quarter i's, odd tokens' G further
-                m[g] = kNone;
-                sum[g] = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4 * kPar; ++i) m[g] = fmaxf(m[g], gm[(i & 3) * kV + (i >> 2) * G]);
-#pragma unroll
-                for (int i = 0; i < 4 * kPar; ++i) {
-                    const float mi = gm[(i & 3) * kV + (i >> 2) * G], li = gl[(i & 3) * kV + (i >> 2) * G];
-                    sum[g] += li * fast_exp2(mi - m[g]);  // (a NaN query's sum is NaN)
-                }
-                o[g] *= fast_exp2(m_o[g] - m[g]);
+                o[g] *= fast_exp2(m_o[g] - __shfl_sync(0xffffffffu, m, g * kEnt));
                 if (kPar == 2 && r >= D) red_o[(g0 + g) * D + r - D] = o[g];
             }
             if constexpr (kPar == 2) named_bar_sync(1, kSoftmaxThreads);
-            if (r < D) {
+            if (p.partition_size && quarter == 0 && ent == 0 && lane < kOG * kEnt && g0 + hg < g_valid)
+                *reinterpret_cast<float2 *>(p.ws_ml + ((row0 + g0 + hg) * p.max_parts + part) * 2) = make_float2(m, sum);
 #pragma unroll
-                for (int g = 0; g < kOG; ++g) {
-                    if (g0 + g >= g_valid) continue;
-                    if constexpr (kPar == 2) o[g] += red_o[(g0 + g) * D + r];
-                    const size_t row = row0 + g0 + g;
-                    if (p.partition_size) {
-                        const size_t at = row * p.max_parts + part;
-                        p.ws_acc[at * D + r] = o[g] * (1.f / kWUnit);
-                        if (r == 0) {
-                            p.ws_ml[at * 2] = m[g];  // log2 units
-                            p.ws_ml[at * 2 + 1] = sum[g];
-                        }
-                    } else {
-                        const float y = sum[g] != 0.f ? o[g] / (sum[g] * kWUnit) : 0.f;
-                        store_out(p.out, row * D + r, y, p.out_dtype);
-                    }
-                }
+            for (int g = 0; g < kOG; ++g) {
+                const float f = __shfl_sync(0xffffffffu, unit, g * kEnt);
+                if (r >= D || g0 + g >= g_valid) continue;
+                if constexpr (kPar == 2) o[g] += red_o[(g0 + g) * D + r];
+                const size_t row = row0 + g0 + g;
+                if (p.partition_size) p.ws_acc[(row * p.max_parts + part) * D + r] = o[g] * f;
+                else store_out(p.out, row * D + r, o[g] * f, p.out_dtype);
             }
             // (the sums are read before the next weights are written: the next item's first barrier is in between)
         }
