@@ -145,12 +145,13 @@ template <int V> struct Shape {
     static constexpr int kOffK = 0;
     static constexpr int kOffV = kOffK + kStages * kTile;
     static constexpr int kOffQ = kOffV + kStages * kTile;      // [kItems] signed digits
-    static constexpr int kOffP = kOffQ + kItems * kDigits;     // unsigned digits; between items the threads' sums
+    static constexpr int kOffP = kOffQ + kItems * kDigits;     // unsigned digits; at an item's end at head_dim 64 the odd tokens' sums
     static constexpr int kOffScales = kOffP + kDigits;
     static constexpr int kOffItems = kOffScales + kScales * (int)sizeof(Scales);
     static constexpr int kOffQs = kOffItems + kItems * (int)sizeof(Item);  // float [kItems][V]: log2 score per digit unit
     static constexpr int kOffMax = (kOffQs + kItems * V * 4 + 15) / 16 * 16;  // float [2][4 warps][V], tiles in turn
-    static constexpr int kOffClc = (kOffMax + 8 * V * 4 + 15) / 16 * 16;
+    static constexpr int kOffSums = (kOffMax + 8 * V * 4 + 15) / 16 * 16;  // float [2][4 warps][V]: the threads' sums
+    static constexpr int kOffClc = (kOffSums + 8 * V * 4 + 15) / 16 * 16;
     static constexpr int kOffBar = kOffClc + 16;
     static constexpr int kBars = 4 * kStages + 2 + 3 + 3 * kItems + 1;
     static constexpr int kEnd = kOffBar + kBars * 8 + 24;  // and tensor memory's address, flags, the hook's wait limit
@@ -166,15 +167,15 @@ template <int V> struct Shape {
     static_assert(kRegsLow + kTeams * kRegsHigh <= (kTeams + 1) * kRegs, "registers taken over are registers given up");
     static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "CTAs per SM");
     static_assert(kCtas * kCols <= 512 && (kCtas + 1) * kRegs * kThreads > 65536, "tensor memory for every resident CTA");
-    static_assert(8 * V * 4 + (V > 1 ? V / 2 : 1) * 64 * 4 <= kDigits, "the threads' sums fit the weights' digits");
+    static_assert((V / 2) * 64 * 4 <= kDigits, "the odd tokens' sums fit the weights' digits");
 };
 
 // ------------------------------------------------------------- tensor cores
 
-// Shared-memory matrix descriptor, 128-byte swizzle, 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc128(uint32_t addr) {
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
+// Shared-memory matrix descriptor, 128-byte swizzle, 8-row groups 1024 bytes
+// apart: its low word for an address, and its high word.
+__device__ __forceinline__ uint32_t desc128(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | (1u << 16); }
+constexpr uint32_t kDescHigh = 64u | (1u << 14) | (2u << 29);
 
 // Instruction descriptor of kind::i8, int32 sums, A signed, M 128.
 __host__ __device__ constexpr uint32_t idesc_i8(bool b_signed, bool a_mn_major, int N) {
@@ -182,12 +183,15 @@ __host__ __device__ constexpr uint32_t idesc_i8(bool b_signed, bool a_mn_major, 
            ((uint32_t)(N >> 3) << 17) | (8u << 24);
 }
 
-__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// a and b: the descriptors' low words; the high words are the same for all.
+__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "mov.b64 a, {%1, %5};\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], a, b, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"((int)kDescHigh)
         : "memory");
 }
 
@@ -367,6 +371,15 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
     const int bs_shift = p.bs_shift;
     const int blocks = kTok >> bs_shift;      // per tile: 4, 8 or 16
     const int rows = 128 / blocks;            // 128-byte rows of a block
+    // mbar_wait that also ends when another warp has given up (looked at only while it spins)
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t t0 = global_ns();
+        for (uint32_t i = 1;; ++i) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if ((i & 63u) == 0u && (*abort_flag || global_ns() - t0 > (wl ? *wl : kWaitLimitNs))) return false;
+        }
+    };
     auto give_up = [&]() {
         record_error(p.err, PA_DEVERR_TIMEOUT);
         *abort_flag = 1;
@@ -426,7 +439,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                 Item &it = items[slot];
                 auto slot_free = [&]() {
                     if (n >= kItems)
-                        sound = __all_sync(0xffffffffu, mbar_wait(i_empty + slot, (n / kItems - 1) & 1, wl) && !*abort_flag);
+                        sound = __all_sync(0xffffffffu, wait(i_empty + slot, (n / kItems - 1) & 1));
                     return sound;
                 };
                 bool asked = false;
@@ -578,7 +591,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                     sound = __all_sync(0xffffffffu, sound && !*abort_flag);
                     if (!sound) break;
                     if (!asked) claim();
-                    sound = __all_sync(0xffffffffu, mbar_wait(clc, claims & 1, wl));
+                    sound = __all_sync(0xffffffffu, wait(clc, claims & 1));
                     ++claims;
                     if (sound) more = canceled(sm + Sh::kOffClc, x, y, z);
                     __syncwarp();
@@ -597,7 +610,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
             bool sound = true;
             for (int n = 0; sound; ++n) {
                 const int slot = n % kItems;
-                sound = __all_sync(0xffffffffu, mbar_wait(i_full + slot, (n / kItems) & 1, wl) && !*abort_flag);
+                sound = __all_sync(0xffffffffu, wait(i_full + slot, (n / kItems) & 1));
                 if (!sound) break;
                 const Item &it = items[slot];
                 const int ntiles = it.ntiles;
@@ -621,7 +634,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                 for (int j = 0; j < ntiles; ++j, ++t) {
                     const int b = t % kStages;
                     if (t >= kStages) {
-                        sound = __all_sync(0xffffffffu, mbar_wait(empty + b, (t / kStages - 1) & 1, wl) && !*abort_flag);
+                        sound = __all_sync(0xffffffffu, wait(empty + b, (t / kStages - 1) & 1));
                         if (!sound) break;
                     }
                     const bool here = lane < blocks && b0 + j * blocks + lane < nblk;
@@ -672,7 +685,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                         // ended whose O is still to be issued here, so that goes first.
                         const int next = (n + 1) % kItems;
                         if (done == issued || mbar_test(q_full + next, ((n + 1) / kItems) & 1)) {
-                            sound = mbar_wait(q_full + next, ((n + 1) / kItems) & 1, wl) && !*abort_flag;
+                            sound = wait(q_full + next, ((n + 1) / kItems) & 1);
                             if (!sound) break;
                             if (n >= 0) mbar_arrive(i_empty + slot);
                             ++n;
@@ -690,11 +703,12 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                     if (!take_s && !take_o) break;  // no more items (with some, the next one was taken above)
                     const int bs = issued % kStages, bo = done % kStages;
                     if (take_s && take_o) {
-                        const uint64_t t0 = global_ns();
+                        uint64_t t0 = 0;
                         for (uint32_t i = 1;; ++i) {
                             take_s = mbar_test(k_full + bs, (issued / kStages) & 1);
                             take_o = !take_s && mbar_test(p_full, done & 1) && mbar_test(v_full + bo, (done / kStages) & 1);
                             if (take_s || take_o) break;
+                            if (i == 64u) t0 = global_ns();
                             if ((i & 63u) == 0u && (*abort_flag || global_ns() - t0 > (wl ? *wl : kWaitLimitNs))) {
                                 sound = false;
                                 break;
@@ -704,13 +718,14 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                     }
                     if (take_s) {
                         const int b = bs;
-                        sound = mbar_wait(k_full + b, (issued / kStages) & 1, wl) && !*abort_flag;
+                        sound = wait(k_full + b, (issued / kStages) & 1);
                         if (!sound) break;
                         fence_after();
-                        const uint32_t ka = base + Sh::kOffK + b * kTile, qa = base + Sh::kOffQ + slot * Sh::kDigits;
+                        const uint32_t ka = desc128(base + Sh::kOffK) + b * (kTile / 16);
+                        const uint32_t qa = desc128(base + Sh::kOffQ) + slot * (Sh::kDigits / 16);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_i8(tmem + Sh::kSCol + (issued & 1) * kN, desc128(ka + kk * 32), desc128(qa + kk * 32), kIdQK,
+                            mma_i8(tmem + Sh::kSCol + (issued & 1) * kN, ka + kk * 2, qa + kk * 2, kIdQK,
                                    kk > 0);
                         mma_commit(s_full + (issued & 1));
                         mma_commit(k_empty + b);
@@ -719,13 +734,13 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                         continue;
                     }
                     const int b = bo;
-                    sound = mbar_wait(p_full, done & 1, wl) && mbar_wait(v_full + b, (done / kStages) & 1, wl) && !*abort_flag;
+                    sound = wait(p_full, done & 1) && wait(v_full + b, (done / kStages) & 1);
                     if (!sound) break;
                     fence_after();
-                    const uint32_t va = base + Sh::kOffV + b * kTile, pa_ = base + Sh::kOffP;
+                    const uint32_t va = desc128(base + Sh::kOffV) + b * (kTile / 16), pa_ = desc128(base + Sh::kOffP);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_i8(tmem + Sh::kOCol, desc128(va + kk * 32 * kRowBytes), desc128(pa_ + kk * 32), kIdPV, kk > 0);
+                        mma_i8(tmem + Sh::kOCol, va + kk * (32 * kRowBytes / 16), pa_ + kk * 2, kIdPV, kk > 0);
                     mma_commit(o_full);
                     mma_commit(v_empty + b);
                     ++done;
@@ -746,20 +761,22 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
         const int v0 = (warp >> 2) * kSV;                     // this thread's first virtual head,
         const int g0 = (warp >> 2) * kOG;                     // its first head in O,
         const int vo = (kPar == 2 ? (quarter >> 1) * G : 0) + g0;  // and that one's virtual head (of the lane's head dim)
-        float *red_m = reinterpret_cast<float *>(Ps), *red_l = red_m + 4 * kV;
-        float *red_o = red_l + 4 * kV;  // [G][64]: the odd tokens' sums at head_dim 64
+        float *red_m = reinterpret_cast<float *>(sm + Sh::kOffSums), *red_l = red_m + 4 * kV;  // [4 warps][kV]
+        // at head_dim 64 the odd tokens' sums, [G][64], where the weights' digits were
+        float *red_o = reinterpret_cast<float *>(Ps);
         int t = 0;                      // tiles done, over all items
         // The warps leave the loops together: one whose wait ran out says so at
-        // the next barrier of all.
-        bool ok = true;
+        // the next barrier of all (each tile has one, each item's end and the end of all).
+        bool ok = true, sound = true;
         for (int n = 0; ok; ++n) {
             const int slot = n % kItems;
-            bool sound = __all_sync(0xffffffffu, mbar_wait(q_full + slot, (n / kItems) & 1, wl) && !*abort_flag);
-            ok = sync_and<kSoftmaxThreads>(sound);
-            if (!ok) break;
+            sound = __all_sync(0xffffffffu, sound && wait(q_full + slot, (n / kItems) & 1));
             const Item &it = items[slot];
-            const int ntiles = it.ntiles;
-            if (ntiles < 0) break;
+            const int ntiles = sound ? it.ntiles : -1;
+            if (ntiles < 0) {
+                ok = sync_and<kSoftmaxThreads>(sound);
+                break;
+            }
             const int L = it.end, first = it.first, part = it.part;
             const size_t row0 = (size_t)it.s * p.num_heads + it.head0;  // output row of head 0
             const int g_valid = min(G, p.group - it.head0 % p.group / kG * kG);
@@ -795,7 +812,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
             };
             for (int j = 0; j < ntiles; ++j, ++t) {
                 float *wm = wmax + (t & 1) * 4 * kV;
-                sound = __all_sync(0xffffffffu, sound && mbar_wait(s_full + (t & 1), (t >> 1) & 1, wl) && !*abort_flag);
+                sound = __all_sync(0xffffffffu, sound && wait(s_full + (t & 1), (t >> 1) & 1));
                 float x[kSV];  // log2 of the weight
                 if (sound) {
                     fence_after();
@@ -868,7 +885,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
 #pragma unroll
                 for (int v = 0; v < kSV; ++v) mt[v] = fmaxf(mt[v], kNone);  // finite, though the weights all be 0
                 if (j > 0) {  // O of the tile before is there: P and O are free once it is added up
-                    sound = __all_sync(0xffffffffu, mbar_wait(o_full, (t - 1) & 1, wl) && !*abort_flag);
+                    sound = __all_sync(0xffffffffu, wait(o_full, (t - 1) & 1));
                     if (!sound) continue;  // (the next barrier tells the others)
                     fence_after();
                     add_tile();
@@ -899,57 +916,63 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                 mbar_arrive(p_full);
             }
             if (!ok) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(i_empty + slot);  // its last S has been read
+            // ---- the threads' sums, while the last product runs
             if (ntiles > 0) {
-                sound = __all_sync(0xffffffffu, sound && mbar_wait(o_full, (t - 1) & 1, wl) && !*abort_flag);
-                if (sound) {
-                    fence_after();
-                    add_tile();
+#pragma unroll
+                for (int v = 0; v < kSV; ++v) {
+                    const float mw = warp_max(m_l[v]);
+                    l[v] *= fast_exp2(m_l[v] - mw);
+                    if (lane == 0) red_m[quarter * kV + v0 + v] = mw;
                 }
+                warp_sums<kSV, 16>(l, lane);  // lane c * 32 / kSV holds head c's
+                if (lane % (32 / kSV) == 0) red_l[quarter * kV + v0 + lane / (32 / kSV)] = l[0];
                 ok = sync_and<kSoftmaxThreads>(sound);
                 if (!ok) break;
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(i_empty + slot);
-            // ---- the threads' sums, where the weights' digits were (their product is done), and the output
-#pragma unroll
-            for (int v = 0; v < kSV; ++v) {
-                const float mw = warp_max(m_l[v]);
-                l[v] *= fast_exp2(m_l[v] - mw);
-                if (lane == 0) red_m[quarter * kV + v0 + v] = mw;
-            }
-            warp_sums<kSV, 16>(l, lane);  // lane c * 32 / kSV holds head c's
-            if (lane % (32 / kSV) == 0) red_l[quarter * kV + v0 + lane / (32 / kSV)] = l[0];
-            named_bar_sync(1, kSoftmaxThreads);
             // lane g * kEnt + i: entry i of head g (its four quarters, twice at head_dim 64)
             constexpr int kEnt = 4 * kPar;
             const int hg = min(lane / kEnt, kOG - 1), ent = lane % kEnt;
             const int at = (ent & 3) * kV + (ent >> 2) * G + g0 + hg;
-            const float mi = red_m[at];
+            const float mi = ntiles > 0 ? red_m[at] : kNone;
             float m = mi;
 #pragma unroll
             for (int i = kEnt / 2; i; i /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
-            float sum = red_l[at] * fast_exp2(mi - m);  // (a NaN query's sum is NaN)
+            float sum = ntiles > 0 ? red_l[at] * fast_exp2(mi - m) : 0.f;  // (a NaN query's sum is NaN)
 #pragma unroll
             for (int i = kEnt / 2; i; i /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, i);
             const float unit = p.partition_size ? 1.f / kWUnit : sum != 0.f ? 1.f / (sum * kWUnit) : 0.f;
+            if (p.partition_size && quarter == 0 && ent == 0 && lane < kOG * kEnt && g0 + hg < g_valid)
+                *reinterpret_cast<float2 *>(p.ws_ml + ((row0 + g0 + hg) * p.max_parts + part) * 2) = make_float2(m, sum);
+            // ---- the last tile, and the output
+            if (ntiles > 0) {
+                sound = __all_sync(0xffffffffu, wait(o_full, (t - 1) & 1));
+                if (sound) {
+                    fence_after();
+                    add_tile();
+                }
+            }
 #pragma unroll
             for (int g = 0; g < kOG; ++g) {
                 o[g] *= fast_exp2(m_o[g] - __shfl_sync(0xffffffffu, m, g * kEnt));
-                if (kPar == 2 && r >= D) red_o[(g0 + g) * D + r - D] = o[g];
+                if (kPar == 2 && ntiles > 0 && r >= D) red_o[(g0 + g) * D + r - D] = o[g];
             }
-            if constexpr (kPar == 2) named_bar_sync(1, kSoftmaxThreads);
-            if (p.partition_size && quarter == 0 && ent == 0 && lane < kOG * kEnt && g0 + hg < g_valid)
-                *reinterpret_cast<float2 *>(p.ws_ml + ((row0 + g0 + hg) * p.max_parts + part) * 2) = make_float2(m, sum);
+            if (kPar == 2 && ntiles > 0) {
+                ok = sync_and<kSoftmaxThreads>(sound);
+                if (!ok) break;
+            }
+            if (!sound) continue;
 #pragma unroll
             for (int g = 0; g < kOG; ++g) {
                 const float f = __shfl_sync(0xffffffffu, unit, g * kEnt);
                 if (r >= D || g0 + g >= g_valid) continue;
-                if constexpr (kPar == 2) o[g] += red_o[(g0 + g) * D + r];
+                if (kPar == 2 && ntiles > 0) o[g] += red_o[(g0 + g) * D + r];
                 const size_t row = row0 + g0 + g;
                 if (p.partition_size) p.ws_acc[(row * p.max_parts + part) * D + r] = o[g] * f;
                 else store_out(p.out, row * D + r, o[g] * f, p.out_dtype);
             }
-            // (the sums are read before the next weights are written: the next item's first barrier is in between)
+            // (the sums are read before the next ones or weights are written: the next tile's barrier is in between)
         }
         if (!ok && tid == 0) give_up();
     }

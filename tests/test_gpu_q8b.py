@@ -7,9 +7,10 @@ with the oracle's attention in double precision over the dequantized cache.
 
 Tolerance of decode, relative to the largest |V| row element M that a sequence
 sees. A score is a sum of D products with q's elements rounded to 2^-22 of the
-power of two of the head's largest one (most are exact), computed within 2^-20 of A = scale * log2(e) * sum_d |q_d k_d|, and
-exp2's own error is below 2^-20: every weight is off by at most
-ln2 * A * 2^-20 + 2^-20, relative. A weighted mean moves by at most twice the
+power of two of the head's largest one (most are exact), computed within 2^-20
+of A = scale * log2(e) * sum_d |q_d k_d|, and exp2's own error is below 2^-20:
+every weight is off by at most ln2 * A * 2^-20 + 2^-20, relative. A weighted
+mean moves by at most twice the
 largest relative error of its weights times M. Weights held in 23 bits of a
 tile's largest one, 128 to a tile, lose another 2^-17 M; fp32 sums over L
 terms, a few 2^-24 sqrt(L). So
