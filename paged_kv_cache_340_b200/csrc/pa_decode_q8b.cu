@@ -965,12 +965,19 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
             if (!sound) continue;
 #pragma unroll
             for (int g = 0; g < kOG; ++g) {
-                const float f = __shfl_sync(0xffffffffu, unit, g * kEnt);
-                if (r >= D || g0 + g >= g_valid) continue;
-                if (kPar == 2 && ntiles > 0) o[g] += red_o[(g0 + g) * D + r];
-                const size_t row = row0 + g0 + g;
-                if (p.partition_size) p.ws_acc[(row * p.max_parts + part) * D + r] = o[g] * f;
-                else store_out(p.out, row * D + r, o[g] * f, p.out_dtype);
+                if (kPar == 2 && ntiles > 0 && r < D) o[g] += red_o[(g0 + g) * D + r];
+                o[g] *= __shfl_sync(0xffffffffu, unit, g * kEnt);
+            }
+            if (r < D) {  // (a loop for each type: a choice within one costs its instructions' fetch eight times)
+                const size_t row = row0 + g0;
+                auto put = [&](auto *to, size_t step) {
+#pragma unroll
+                    for (int g = 0; g < kOG; ++g)
+                        if (g0 + g < g_valid) to[g * step] = (std::remove_pointer_t<decltype(to)>)o[g];
+                };
+                if (p.partition_size) put(p.ws_acc + (row * p.max_parts + part) * D + r, (size_t)p.max_parts * D);
+                else if (p.out_dtype == PA_F32) put(static_cast<float *>(p.out) + row * D + r, D);
+                else put(static_cast<T *>(p.out) + row * D + r, D);
             }
             // (the sums are read before the next ones or weights are written: the next tile's barrier is in between)
         }
