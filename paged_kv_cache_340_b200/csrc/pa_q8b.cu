@@ -33,26 +33,35 @@ struct AppendParams {
 
 constexpr int kWarps = 8;
 
-template <typename T, int D, int BS> struct AppendShape {
+template <typename T, int D, int BS, bool kByToken> struct AppendShape {
     static constexpr int kVec = 16 / sizeof(T);  // values of a lane's vector
     static constexpr int kLanes = D / kVec;      // lanes of a row
     static constexpr int kRows = 32 / kLanes;    // rows per warp load
-    // warps that share a block, so that its rows take at most 64 registers of a
-    // lane (a warp alone with 128 took 143 us where the pair takes 109: prompts
-    // of 2048 fp32 tokens, 32 heads of 128, blocks of 32)
-    static constexpr int kTeam = BS / kRows > 16 ? 2 : 1;
+    // Warps that share a block. Two above 16 loads of a warp, so that its rows
+    // take at most 64 registers of a lane (a warp alone with 128 took 143 us where
+    // the pair takes 109: prompts of 2048 fp32 tokens, 32 heads of 128, blocks of
+    // 32); and above 8, which leaves room for a fourth CTA (100 ragged chunks, 6
+    // fp32 heads of 64: 23.1 -> 21.0 us, 20 of up to 1000 bf16 tokens 15.9 ->
+    // 14.7), but not for a few rows a block, which a warp takes in one load (256
+    // single tokens: 8.6 us, 10.6 in pairs).
+    static constexpr int kTeam = BS / kRows > (kByToken ? 16 : 8) ? 2 : 1;
     static constexpr int kIt = BS / kRows / kTeam;  // loads of a warp per full block
     static constexpr int kCtas = kIt <= 8 ? 4 : 3;
 };
 
-// Sequence s touches at most q_len / bs + 2 blocks, so numbering its blocks
-// from first_unit(q_start[s], s) on gives every block of every sequence a unit
-// of its own without a scan; a few units are empty.
-template <int BS> __device__ __forceinline__ int first_unit(int q0, int s) { return q0 / BS + 2 * s; }
+// The units of work are a sequence's blocks with new rows. Numbering them must
+// need no scan: a sequence touches at most q_len / bs + 2 blocks, so counting
+// from q_start[s] / bs + 2 s on gives every block a unit of its own, and a few
+// units are empty. With few tokens a sequence, where that is fewer, a block's
+// unit is its first new token instead: none is empty for single tokens (256 of
+// them: 8.7 -> 7.1 us with blocks of 32, 6.6 -> 4.6 with 16).
+template <int BS, bool kByToken> __device__ __forceinline__ int first_unit(int q0, int s) {
+    return kByToken ? q0 : q0 / BS + 2 * s;
+}
 
 // The largest s with first_unit(q_start[s], s) <= u, searched by the warp 128
 // ways at a time, so that up to 128 sequences take one round of loads.
-template <int BS> __device__ __forceinline__ int unit_seq(const int32_t *q_start, int n, int u, int lane) {
+template <int BS, bool kByToken> __device__ __forceinline__ int unit_seq(const int32_t *q_start, int n, int u, int lane) {
     constexpr int kWays = 4;  // probes a lane
     int lo = 0;
     while (n > 1) {
@@ -61,7 +70,7 @@ template <int BS> __device__ __forceinline__ int unit_seq(const int32_t *q_start
 #pragma unroll
         for (int i = 0; i < kWays; ++i) {
             const int k = (i * 32 + lane) * step;
-            le[i] = k < n && first_unit<BS>(__ldg(q_start + lo + min(k, n - 1)), lo + k) <= u;
+            le[i] = k < n && first_unit<BS, kByToken>(__ldg(q_start + lo + min(k, n - 1)), lo + k) <= u;
         }
         int last = 0;
 #pragma unroll
@@ -117,9 +126,10 @@ template <typename T> struct Magnitude {
 // 4 instructions a value leave the loads the bound (a first version with
 // conversions and clamps and one (head, K or V) a warp took 99 us where this
 // one takes 67 for eight fp16 prompts of 2048 tokens and 32 heads, 403 MB).
-template <typename T, int D, int BS>
-__global__ void __launch_bounds__(kWarps * 32, AppendShape<T, D, BS>::kCtas) append_kernel(const AppendParams p) {
-    using Sh = AppendShape<T, D, BS>;
+template <typename T, int D, int BS, bool kByToken>
+__global__ void __launch_bounds__(kWarps * 32, AppendShape<T, D, BS, kByToken>::kCtas)
+    append_kernel(const AppendParams p) {
+    using Sh = AppendShape<T, D, BS, kByToken>;
     using Mag = Magnitude<T>;
     constexpr int kVec = Sh::kVec, kLanes = Sh::kLanes, kRows = Sh::kRows, kIt = Sh::kIt, kTeam = Sh::kTeam;
     wait_previous();
@@ -127,7 +137,7 @@ __global__ void __launch_bounds__(kWarps * 32, AppendShape<T, D, BS>::kCtas) app
     const int lane = threadIdx.x & 31;
     const int H = p.num_kv_heads;
     const int u = blockIdx.x;
-    const int s = unit_seq<BS>(p.q_start, p.num_seqs, u, lane);
+    const int s = unit_seq<BS, kByToken>(p.q_start, p.num_seqs, u, lane);
     const int q0 = __ldg(p.q_start + s), q1 = __ldg(p.q_start + s + 1);
     const int ctx = __ldg(p.ctx + s);
     const bool first_warp = blockIdx.y == 0 && threadIdx.x < 32;
@@ -136,9 +146,10 @@ __global__ void __launch_bounds__(kWarps * 32, AppendShape<T, D, BS>::kCtas) app
         return;
     }
     const int p0 = ctx - (q1 - q0);                        // position of the first new token
-    const int lb = p0 / BS + u - first_unit<BS>(q0, s);    // this unit's logical block
+    const int unit = u - first_unit<BS, kByToken>(q0, s);  // of the sequence
+    const int lb = kByToken ? (p0 + unit) / BS : p0 / BS + unit;  // its logical block
     const int a = max(p0, lb * BS), e = min(ctx, (lb + 1) * BS);
-    if (a >= e) return;
+    if (kByToken ? u >= q1 || a != p0 + unit : a >= e) return;
     const int id = __ldg(p.tables + (size_t)s * p.max_blocks + lb);
     if (id < 0 || id >= p.num_blocks) {
         if (first_warp && lane == 0) record_error(p.err, PA_DEVERR_BLOCK_ID);
@@ -146,7 +157,7 @@ __global__ void __launch_bounds__(kWarps * 32, AppendShape<T, D, BS>::kCtas) app
     }
     const int o0 = a - lb * BS, n = e - a;  // the new rows are slots o0 .. o0 + n - 1 of the block
     const int warp = threadIdx.x >> 5, part = warp % kTeam;
-    const int row = part * kIt * kRows + lane / kLanes, col = (lane % kLanes) * kVec;
+    const int row = part * kRows + lane / kLanes, col = (lane % kLanes) * kVec;
     // the largest of the team's warps; two slots a warp, used in turn
     __shared__ uint32_t team_mag[2][kWarps];
     int turn = 0;
@@ -169,8 +180,8 @@ __global__ void __launch_bounds__(kWarps * 32, AppendShape<T, D, BS>::kCtas) app
         const float old = o0 > 0 ? *scale : 0.f;
 
         auto load = [&](int i) -> uint4 {
-            const int r = i * kRows + row;
-                        return r < n ? __ldg(reinterpret_cast<const uint4 *>(src + (size_t)r * H * D)) : make_uint4(0u, 0u, 0u, 0u);
+            const int r = i * kTeam * kRows + row;
+            return r < n ? __ldg(reinterpret_cast<const uint4 *>(src + (size_t)r * H * D)) : make_uint4(0u, 0u, 0u, 0u);
         };
         uint4 held[kIt];
         uint32_t mag = 0;
@@ -201,7 +212,7 @@ __global__ void __launch_bounds__(kWarps * 32, AppendShape<T, D, BS>::kCtas) app
         const float inv = now > 0.f ? __fdiv_rn(1.f, now) : 0.f;
 #pragma unroll
         for (int i = 0; i < kIt; ++i) {
-            const int r = i * kRows + row;
+            const int r = i * kTeam * kRows + row;
             if (r >= n) continue;
             float x[kVec];
             Elt<T>::unpack(held[i], x);
@@ -255,20 +266,28 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-template <typename T>
-static cudaError_t launch_append_t(const AppendParams &p, int head_dim, int block_size, cudaStream_t stream) {
-    const long long units = (long long)p.num_tokens / block_size + 2ll * p.num_seqs + 1;
+template <typename T, int D, int BS, bool kByToken>
+static cudaError_t launch_append_as(const AppendParams &p, long long units, cudaStream_t stream) {
     // (head, K or V) pairs a warp takes one after another: two where 8 CTAs
     // an SM are left, which halves the lookups (1, 2, 3 and 4 took 69.4, 67.0,
     // 66.5 and 67.5 us for prompts of 2048 tokens and 32 heads)
-    const int team = sizeof(T) == 4 && head_dim == 128 && block_size == 32 ? AppendShape<float, 128, 32>::kTeam : 1;
-    const int warps_y = (2 * p.num_kv_heads * team + kWarps - 1) / kWarps;
+    const int warps_y = (2 * p.num_kv_heads * AppendShape<T, D, BS, kByToken>::kTeam + kWarps - 1) / kWarps;
     long long per = units * warps_y / (8ll * sm_count());
     per = per < 1 ? 1 : per > 2 ? 2 : per;
     const dim3 grid((unsigned)units, (unsigned)((warps_y + per - 1) / per));
-    auto kern = head_dim == 128 ? (block_size == 16 ? append_kernel<T, 128, 16> : append_kernel<T, 128, 32>)
-                                : (block_size == 16 ? append_kernel<T, 64, 16> : append_kernel<T, 64, 32>);
-    return launch_after(kern, grid, kWarps * 32, 0, 1, stream, p);
+    return launch_after(append_kernel<T, D, BS, kByToken>, grid, kWarps * 32, 0, 1, stream, p);
+}
+
+template <typename T, int D, int BS> static cudaError_t launch_append_n(const AppendParams &p, cudaStream_t stream) {
+    const long long units = (long long)p.num_tokens / BS + 2ll * p.num_seqs + 1;
+    return p.num_tokens < units ? launch_append_as<T, D, BS, true>(p, p.num_tokens, stream)
+                                : launch_append_as<T, D, BS, false>(p, units, stream);
+}
+
+template <typename T>
+static cudaError_t launch_append_t(const AppendParams &p, int head_dim, int block_size, cudaStream_t stream) {
+    return head_dim == 128 ? (block_size == 16 ? launch_append_n<T, 128, 16>(p, stream) : launch_append_n<T, 128, 32>(p, stream))
+                           : (block_size == 16 ? launch_append_n<T, 64, 16>(p, stream) : launch_append_n<T, 64, 32>(p, stream));
 }
 
 static bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

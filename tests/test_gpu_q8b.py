@@ -139,6 +139,25 @@ def test_write_is_bit_exact(pa, dtype, H, D, bs, k):
     c.check(pa, d)
 
 
+@pytest.mark.parametrize("more", [-1, 0, 1])
+@pytest.mark.parametrize("dtype,D,bs", [(torch.float16, 128, 32), (torch.float32, 64, 16), (torch.bfloat16, 64, 32)])
+def test_write_few_and_many_tokens_a_sequence(pa, dtype, D, bs, more):
+    """Work is dealt out by tokens or by blocks, whichever are fewer: both, on
+    either side of the point where they are as many (by padding), with long,
+    single-token and empty sequences in one batch and more than 128 of them."""
+    rng = np.random.default_rng(77)
+    S = 150
+    new = rng.integers(0, 2, S)
+    new[[3, 70, 149]] = [101, 2 * bs, bs + 1]
+    old = rng.integers(0, 3 * bs, S)
+    T = int(new.sum())
+    pad = next(k for k in range(10000) if T + k >= (T + k) // bs + 2 * S + 1) + more
+    c = WriteCase(2, D, bs, dtype, old, new, seed=78, pad=pad)
+    d = c.run(pa)
+    assert pa.pa_read_device_errors() == 0
+    c.check(pa, d)
+
+
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
 def test_write_extreme_values(pa, dtype):
     """Zero blocks, NaN and infinities (kept out of the scale), the type's
