@@ -277,6 +277,30 @@ __device__ __forceinline__ float number(int hi, int mid, int lo) {
     return fmaf(h, 65536.f, (float)(mid * 256 + lo));
 }
 
+// Two at a time: sums and products of pairs are one instruction each.
+struct Pair {
+    uint64_t v;
+    __device__ __forceinline__ Pair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ explicit Pair(float a) : Pair(a, a) {}
+    __device__ __forceinline__ void get(float &a, float &b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(a.v) : "l"(a.v), "l"(b.v));
+    return a;
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(a.v) : "l"(a.v), "l"(b.v));
+    return a;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(a.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return a;
+}
+__device__ __forceinline__ Pair number2(const int *c) {
+    const Pair h = Pair(__int_as_float(0x4b400000 + c[0]), __int_as_float(0x4b400000 + c[3])) + Pair(-12582912.f);
+    return fma2(h, Pair(65536.f), Pair((float)(c[1] * 256 + c[2]), (float)(c[4] * 256 + c[5])));
+}
+
 __device__ __forceinline__ float warp_max(float x) {
     float y;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
@@ -799,9 +823,15 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
             auto add_tile = [&]() {
                 int c[kOCols3];
                 tmem_load<kOCols3>(tlane + Sh::kOCol + 3 * vo, c);
+                float f2[2];
 #pragma unroll
                 for (int g = 0; g < kOG; ++g) {
-                    const float f = number(c[3 * g], c[3 * g + 1], c[3 * g + 2]);
+                    if constexpr (kOG % 2 == 0) {
+                        if (g % 2 == 0) number2(c + 3 * g).get(f2[0], f2[1]);
+                    } else {
+                        f2[g % 2] = number(c[3 * g], c[3 * g + 1], c[3 * g + 2]);
+                    }
+                    const float f = f2[g % 2];
                     if (m_tile[g] > m_o[g]) {  // the same in every thread of the warp
                         o[g] = fmaf(o[g], fast_exp2(m_o[g] - m_tile[g]), f);
                         m_o[g] = m_tile[g];
@@ -826,9 +856,15 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                     int c[kCols3];
                     tmem_load<kCols3>(tlane + Sh::kSCol + (t & 1) * kN + 3 * v0, c);
                     float score[kSV];
+                    if constexpr (kSV % 2 == 0) {
 #pragma unroll
-                    for (int v = 0; v < kSV; ++v)
-                        score[v] = number(c[3 * v], c[3 * v + 1], c[3 * v + 2]) * (qs[v] * ks);
+                        for (int v = 0; v < kSV; v += 2)
+                            (number2(c + 3 * v) * (Pair(qs[v], qs[v + 1]) * Pair(ks))).get(score[v], score[v + 1]);
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < kSV; ++v)
+                            score[v] = number(c[3 * v], c[3 * v + 1], c[3 * v + 2]) * (qs[v] * ks);
+                    }
                     if (!whole) {
 #pragma unroll
                         for (int v = 0; v < kSV; ++v)
@@ -836,21 +872,41 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                     }
                     // The sum's reference is a score seen before, raised only when one is
                     // above it by kRaise: a term is then at most 2^kRaise.
-                    float above = -INFINITY;
+                    float above = -INFINITY, over[kSV];  // score - m_l
+                    auto sub = [&](float (&to)[kSV], const float (&a)[kSV], const float (&b)[kSV]) {
+                        if constexpr (kSV % 2 == 0) {
 #pragma unroll
-                    for (int v = 0; v < kSV; ++v) above = fmaxf(above, score[v] - m_l[v]);
+                            for (int v = 0; v < kSV; v += 2)
+                                fma2(Pair(b[v], b[v + 1]), Pair(-1.f), Pair(a[v], a[v + 1])).get(to[v], to[v + 1]);
+                        } else {
+#pragma unroll
+                            for (int v = 0; v < kSV; ++v) to[v] = a[v] - b[v];
+                        }
+                    };
+                    sub(over, score, m_l);
+#pragma unroll
+                    for (int v = 0; v < kSV; ++v) above = fmaxf(above, over[v]);
                     if (above > kRaise) {
 #pragma unroll
                         for (int v = 0; v < kSV; ++v)
-                            if (score[v] - m_l[v] > kRaise) {
-                                l[v] *= fast_exp2(m_l[v] - score[v]);
+                            if (over[v] > kRaise) {
+                                l[v] *= fast_exp2(-over[v]);
                                 m_l[v] = score[v];
+                                over[v] = 0.f;
                             }
                     }
+                    if constexpr (kSV % 2 == 0) {
 #pragma unroll
-                    for (int v = 0; v < kSV; ++v) {
-                        l[v] += fast_exp2(score[v] - m_l[v]);
-                        x[v] = score[v] + lv;
+                        for (int v = 0; v < kSV; v += 2) {
+                            (Pair(l[v], l[v + 1]) + Pair(fast_exp2(over[v]), fast_exp2(over[v + 1]))).get(l[v], l[v + 1]);
+                            (Pair(score[v], score[v + 1]) + Pair(lv)).get(x[v], x[v + 1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < kSV; ++v) {
+                            l[v] += fast_exp2(over[v]);
+                            x[v] = score[v] + lv;
+                        }
                     }
                     // the tile's largest weight per head, over this warp
 #pragma unroll
@@ -899,10 +955,21 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                     for (int g = 0; g < kOG; ++g) m_tile[g] = fmaxf(m_tile[g], kNone);
                 }
                 // ---- the weights' digits, row 3 v + i, byte r of the row (its 16-byte chunks swizzled)
+                // (a whole number is the sum's mantissa: no conversion; bit 23 is 0 in its exponent)
+                float w[kSV];
+                if constexpr (kSV % 2 == 0) {
+#pragma unroll
+                    for (int v = 0; v < kSV; v += 2) {
+                        fma2(Pair(mt[v], mt[v + 1]), Pair(-1.f), Pair(x[v], x[v + 1])).get(w[v], w[v + 1]);
+                        fma2(Pair(fast_exp2(w[v]), fast_exp2(w[v + 1])), Pair(kWUnit), Pair(8388608.f)).get(w[v], w[v + 1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int v = 0; v < kSV; ++v) w[v] = fmaf(fast_exp2(x[v] - mt[v]), kWUnit, 8388608.f);
+                }
 #pragma unroll
                 for (int v = 0; v < kSV; ++v) {
-                    // the whole number is the sum's mantissa: no conversion (bit 23 is 0 in its exponent)
-                    const unsigned u = __float_as_uint(fmaf(fast_exp2(x[v] - mt[v]), kWUnit, 8388608.f));
+                    const unsigned u = __float_as_uint(w[v]);
                     const int d = 3 * v, d0 = 3 * v0;  // (3 v0 is a multiple of 8 with two teams, else 0)
                     static_assert(kTeams == 1 || 3 * kSV % 8 == 0 || kSV == 4, "swizzle phase");
                     const int ph = kTeams == 1 || 3 * kSV % 8 == 0 ? 0 : d0 & 7;
