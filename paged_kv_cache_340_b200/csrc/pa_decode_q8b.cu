@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                 int s = z;
                 bool real = true;  // whether it has an output (else it is dropped)
                 if (p.seq_order) {
-                    s = __ldg(p.seq_order + z);
+                    s = p.seq_order[z];
                     if (s < 0 || s >= p.num_seqs) {
                         if (lane == 0) record_error(p.err, PA_DEVERR_CONTEXT);
                         s = 0;
@@ -506,13 +506,13 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                 for (int g = 0; g < G; ++g) {
                     raw[g] = Raw{};
                     if (g < g_valid)
-                        raw[g] = __ldg(reinterpret_cast<const Raw *>(static_cast<const T *>(p.query) +
-                                                                     ((size_t)s * p.num_heads + head0 + g) * D) + lane);
+                        raw[g] = reinterpret_cast<const Raw *>(static_cast<const T *>(p.query) +
+                                                               ((size_t)s * p.num_heads + head0 + g) * D)[lane];
                 }
                 const int first = x * p.partition_size;
                 const int lb = (first >> bs_shift) + lane;
-                int id = lane < blocks && lb < p.max_blocks ? __ldg(p.tables + (size_t)s * p.max_blocks + lb) : -1;
-                int L = __ldg(p.ctx + s);
+                int id = lane < blocks && lb < p.max_blocks ? p.tables[(size_t)s * p.max_blocks + lb] : -1;
+                int L = p.ctx[s];
                 const int room = (int)min((long long)p.max_blocks << bs_shift, (long long)p.max_ctx);
                 if (real && (L < 0 || L > room)) {
                     if (lane == 0) record_error(p.err, PA_DEVERR_CONTEXT);
@@ -647,11 +647,11 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                 if (lane == 0) mbar_arrive(i_empty + slot);
                 auto look = [&](int j) -> int {
                     const int lb = b0 + j * blocks + lane;
-                    return (lane < blocks && lb < nblk) ? __ldg(trow + lb) : -1;
+                    return (lane < blocks && lb < nblk) ? trow[lb] : -1;
                 };
                 auto scale_of = [&](const float *scale, int block) -> float {
                     return !is_v && block >= 0 && block < p.num_blocks
-                               ? __ldg(scale + (size_t)block * p.num_kv_heads + kvh) : 0.f;
+                               ? scale[(size_t)block * p.num_kv_heads + kvh] : 0.f;
                 };
                 int id_next = ntiles > 1 ? look(1) : -1;
                 float ks = scale_of(p.k_scale, id), vs = scale_of(p.v_scale, id);
@@ -1074,11 +1074,11 @@ template <int D, int kJoinWarps> __global__ void __launch_bounds__(kJoinWarps * 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int s = blockIdx.y;
     if (p.seq_order) {
-        s = __ldg(p.seq_order + s);
+        s = p.seq_order[s];
         if (s < 0 || s >= p.num_seqs) return;  // recorded by decode_kernel
     }
     const long long room = min((long long)p.max_blocks << p.bs_shift, (long long)p.max_ctx);
-    const int L = (int)min((long long)max(__ldg(p.ctx + s), 0), room);
+    const int L = (int)min((long long)max(p.ctx[s], 0), room);
     const int n = (L + p.partition_size - 1) / p.partition_size;
     const size_t row = (size_t)s * p.num_heads + blockIdx.x;
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml) + row * p.max_parts;

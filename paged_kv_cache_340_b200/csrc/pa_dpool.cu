@@ -185,7 +185,7 @@ template <int kPer> __global__ void __launch_bounds__(kThreads, 1) append_kernel
         ctx[i] = nw[i] = 0;
         if (s0 + i < s1) {
             ctx[i] = __ldcg(q.ctx + s0 + i);
-            nw[i] = __ldg(q.new_lens + s0 + i);
+            nw[i] = __ldcg(q.new_lens + s0 + i);
         }
     }
     int bad = 0;  // PA_DEVERR_* bits
@@ -403,7 +403,7 @@ template <int kPer> __global__ void __launch_bounds__(kThreads, 1) release_kerne
         n[i] = 0;
         if (s0 + i < s1) {
             n[i] = __ldcg(q.ctx + s0 + i);
-            gone |= (unsigned)(__ldg(q.finished + s0 + i) != 0) << i;
+            gone |= (unsigned)(__ldcg(q.finished + s0 + i) != 0) << i;
         }
     }
     int bad = 0;  // PA_DEVERR_* bits

@@ -2,7 +2,9 @@
 // up while the kernel before it in the stream still runs. It calls
 // wait_previous() in every thread before it touches global memory (which waits
 // until that kernel, and so all before it, has finished), and allow_next() once
-// its own CTAs have started.
+// its own CTAs have started. What the kernel before may have written is not read
+// with __ldg: its non-coherent loads are for data that no one writes while the
+// kernel runs, and this one does run, though it waits, while the one before writes.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -70,7 +70,7 @@ template <int BS, bool kByToken> __device__ __forceinline__ int unit_seq(const i
 #pragma unroll
         for (int i = 0; i < kWays; ++i) {
             const int k = (i * 32 + lane) * step;
-            le[i] = k < n && first_unit<BS, kByToken>(__ldg(q_start + lo + min(k, n - 1)), lo + k) <= u;
+            le[i] = k < n && first_unit<BS, kByToken>(q_start[lo + min(k, n - 1)], lo + k) <= u;
         }
         int last = 0;
 #pragma unroll
@@ -138,8 +138,8 @@ __global__ void __launch_bounds__(kWarps * 32, AppendShape<T, D, BS, kByToken>::
     const int H = p.num_kv_heads;
     const int u = blockIdx.x;
     const int s = unit_seq<BS, kByToken>(p.q_start, p.num_seqs, u, lane);
-    const int q0 = __ldg(p.q_start + s), q1 = __ldg(p.q_start + s + 1);
-    const int ctx = __ldg(p.ctx + s);
+    const int q0 = p.q_start[s], q1 = p.q_start[s + 1];
+    const int ctx = p.ctx[s];
     const bool first_warp = blockIdx.y == 0 && threadIdx.x < 32;
     if (q0 < 0 || q1 < q0 || q1 > p.num_tokens || q1 - q0 > ctx || ctx > (long long)p.max_blocks * BS) {
         if (first_warp && lane == 0) record_error(p.err, PA_DEVERR_CONTEXT);
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kWarps * 32, AppendShape<T, D, BS, kByToken>::
     const int lb = kByToken ? (p0 + unit) / BS : p0 / BS + unit;  // its logical block
     const int a = max(p0, lb * BS), e = min(ctx, (lb + 1) * BS);
     if (kByToken ? u >= q1 || a != p0 + unit : a >= e) return;
-    const int id = __ldg(p.tables + (size_t)s * p.max_blocks + lb);
+    const int id = p.tables[(size_t)s * p.max_blocks + lb];
     if (id < 0 || id >= p.num_blocks) {
         if (first_warp && lane == 0) record_error(p.err, PA_DEVERR_BLOCK_ID);
         return;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kWarps * 32, AppendShape<T, D, BS, kByToken>::
 
         auto load = [&](int i) -> uint4 {
             const int r = i * kTeam * kRows + row;
-            return r < n ? __ldg(reinterpret_cast<const uint4 *>(src + (size_t)r * H * D)) : make_uint4(0u, 0u, 0u, 0u);
+            return r < n ? *reinterpret_cast<const uint4 *>(src + (size_t)r * H * D) : make_uint4(0u, 0u, 0u, 0u);
         };
         uint4 held[kIt];
         uint32_t mag = 0;
