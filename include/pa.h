@@ -608,8 +608,9 @@ int pa_beam_step_withhold_arrival(void *state, int num_blocks, int block_size, c
  * uninitialised state or one of other sizes) applies nothing: the pool, the
  * tables and the lengths are unchanged, q_start is all 0, every slot and pair
  * -1, *num_cow = 0 and a PA_DEVERR_* bit is set. The arrays must not overlap.
- * One launch; num_seqs <= PA_DPOOL_MAX_SEQS and num_seqs * max_blocks_per_seq
- * < 2^30 (else PA_ERR_SHAPE). Calls on one state must not overlap.
+ * One launch; num_seqs <= PA_DPOOL_MAX_SEQS, num_seqs * max_blocks_per_seq
+ * < 2^30 and max_tokens <= 2^30 (else PA_ERR_SHAPE). Calls on one state must
+ * not overlap.
  */
 #define PA_DPOOL_MAX_SEQS 8192
 int pa_dpool_append(void *state, int num_blocks, int block_size, int32_t *block_tables, int max_blocks_per_seq,

@@ -681,7 +681,7 @@ extern "C" int pa_dpool_append(void *state, int num_blocks, int block_size, int3
                                int32_t *num_cow, cudaStream_t stream) {
     int rc = dpool::check_sizes(num_blocks, block_size, max_blocks_per_seq, num_seqs);
     if (rc != PA_OK) return rc;
-    if (max_tokens < 0) return PA_ERR_SHAPE;
+    if (max_tokens < 0 || max_tokens > (1 << 30)) return PA_ERR_SHAPE;
     if (!state || !q_start || !num_cow || (max_tokens > 0 && !slot_mapping) ||
         (num_seqs > 0 && (!block_tables || !context_lens || !new_lens || !cow_pairs)))
         return PA_ERR_NULL;

@@ -96,3 +96,8 @@ def test_copy_blocks_q8b_host_checks(pa, kw, code):
     a = dict(kc=A, vc=A, ks=A, vs=A, pairs=A, count=None, n=3, nb=40, H=2, D=128, bs=16)
     a.update(kw)
     assert pa._lib.pa_copy_blocks_q8b(*a.values(), None) == code
+
+
+@pytest.mark.parametrize("T", [(1 << 30) + 1, (1 << 31) - 1])
+def test_dpool_append_refuses_more_slots_than_it_can_number(pa, T):
+    assert pa._lib.pa_dpool_append(A, 64, 16, A, 8, A, A, 4, A, A, T, A, A, None) == -3
