@@ -472,16 +472,18 @@ class HostStepPipeline:
 
 
 class ServingStep:
-    """Continuous batching with the whole step on the device, over an int8
-    cache with one scale per (block, kv head).
+    """Continuous batching with the whole step on the device, over num_layers
+    int8 caches with one scale per (block, kv head) and one block table.
 
     num_seqs rows hold the running sequences (a row without one has length 0).
     A step frees the rows marked finished, appends new_lens[s] tokens to each
     row (a prompt, one decoded token, or none), copies the shared blocks it
-    writes into, writes the new K/V rows and decodes every row's last token:
-    the host neither allocates blocks nor reads anything back, and every
-    buffer keeps its size, so a step can be captured in a CUDA graph once and
-    replayed. Its calls go to one stream; steps of one object must not overlap.
+    writes into (schedule: every layer's), then writes a layer's new K/V rows
+    and decodes every row's last token (attend: once per layer and step, since
+    a write takes the rows before its own as they are). The host neither
+    allocates blocks nor reads anything back, and every buffer keeps its size,
+    so a step can be captured in a CUDA graph once and replayed. Its calls go to
+    one stream; steps of one object must not overlap.
 
     A prompt's row is decoded for its last token like any other; rows of
     length 0 give zeros. Check pa_read_device_errors() now and then: a step
@@ -490,7 +492,9 @@ class ServingStep:
     def __init__(self, num_seqs: int, max_blocks_per_seq: int, num_blocks: int, block_size: int, num_heads: int,
                  num_kv_heads: int, head_dim: int, max_tokens: int, dtype: torch.dtype = torch.bfloat16,
                  out_dtype: Optional[torch.dtype] = None, scale: Optional[float] = None, policy: int = PA_POOL_FIFO,
-                 device="cuda", pool: Optional[DevicePool] = None):
+                 device="cuda", pool: Optional[DevicePool] = None, num_layers: int = 1):
+        if num_layers < 1:
+            raise ValueError("ServingStep: at least one layer")
         i32 = dict(dtype=torch.int32, device=device)
         self.pool = pool if pool is not None else DevicePool(num_blocks, block_size, policy, device=device)
         self.block_tables = torch.full((num_seqs, max_blocks_per_seq), -1, **i32)
@@ -500,18 +504,17 @@ class ServingStep:
         self.cow_pairs = torch.empty((num_seqs, 2), dtype=torch.int64, device=device)
         self.num_cow = torch.zeros(1, **i32)
         shape = (num_blocks, num_kv_heads, block_size, head_dim)
-        self.k_cache = torch.zeros(shape, dtype=torch.int8, device=device)
-        self.v_cache = torch.zeros(shape, dtype=torch.int8, device=device)
-        self.k_scale = torch.zeros(shape[:2], dtype=torch.float32, device=device)
-        self.v_scale = torch.zeros(shape[:2], dtype=torch.float32, device=device)
+        kinds = 2 * [(shape, torch.int8)] + 2 * [(shape[:2], torch.float32)]
+        # each layer's k_cache, v_cache, k_scale, v_scale
+        self.layers = [tuple(torch.zeros(sh, dtype=dt, device=device) for sh, dt in kinds) for _ in range(num_layers)]
         self.max_context_len = max_blocks_per_seq * block_size
         nbytes = pa_decode_q8b_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, self.max_context_len)
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.out = torch.empty((num_seqs, num_heads, head_dim), dtype=out_dtype or dtype, device=device)
         self.scale = head_dim ** -0.5 if scale is None else scale
 
-    def cache(self) -> tuple:
-        return self.k_cache, self.v_cache, self.k_scale, self.v_scale
+    def cache(self, layer: int = 0) -> tuple:
+        return self.layers[layer]
 
     def schedule(self, new_lens, finished, stream=None) -> None:
         """The step's pool work: finished rows freed, new tokens given their
@@ -520,18 +523,24 @@ class ServingStep:
         pa_dpool_release(self.pool, self.block_tables, self.context_lens, finished, stream=stream)
         pa_dpool_append(self.pool, self.block_tables, self.context_lens, new_lens, self.q_start, self.slot_mapping,
                         self.cow_pairs, self.num_cow, stream=stream)
-        pa_copy_blocks_q8b(*self.cache(), self.cow_pairs, self.num_cow, stream=stream)
+        for cache in self.layers:
+            pa_copy_blocks_q8b(*cache, self.cow_pairs, self.num_cow, stream=stream)
 
-    def attend(self, key, value, query, stream=None) -> torch.Tensor:
+    def attend(self, key, value, query, stream=None, layer: int = 0) -> torch.Tensor:
         """One layer's part: key and value [max_tokens, Hkv, D] (the new tokens
         row after row, then padding) into the cache, then the attention of
-        query [num_seqs, Hq, D], each row's last token. Returns out."""
-        pa_append_q8b(key, value, self.q_start, *self.cache(), self.block_tables, self.context_lens, stream=stream)
-        pa_decode_q8b(self.out, query, *self.cache(), self.block_tables, self.context_lens, self.scale,
-                      self.max_context_len, self.workspace, stream=stream)
+        query [num_seqs, Hq, D], each row's last token. Returns out (one buffer
+        for all layers)."""
+        cache = self.layers[layer]
+        pa_append_q8b(key, value, self.q_start, *cache, self.block_tables, self.context_lens, stream=stream)
+        pa_decode_q8b(self.out, query, *cache, self.block_tables, self.context_lens, self.scale, self.max_context_len,
+                      self.workspace, stream=stream)
         return self.out
 
     def step(self, new_lens, finished, key, value, query, stream=None) -> torch.Tensor:
+        """schedule and the attend of a single layer."""
+        if len(self.layers) != 1:
+            raise ValueError("ServingStep.step is of one layer: call schedule, then attend for each")
         self.schedule(new_lens, finished, stream)
         return self.attend(key, value, query, stream)
 

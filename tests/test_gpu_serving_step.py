@@ -210,3 +210,41 @@ def test_tables_and_slots_serve_a_16_bit_cache(pa):
         # the acceptance bound of the prefill tests (fp16, fp32 output)
         assert np.abs(f64(out)[:n] - want[:n]).max() <= 4e-3
         assert (out[n:] == 0).all()
+
+
+def test_layers_share_the_step(pa):
+    """Two layers over one block table: forks' copies reach every layer's cache,
+    each layer's write and attention only its own."""
+    from paged_kv_cache_340_b200.batch import ServingStep
+    S, MB, NB, T, bs, Hq, Hkv, D = 4, 6, 40, 60, 16, 4, 2, 64
+    gen = torch.Generator().manual_seed(11)
+    refs = [Reference(pa, S, MB, NB, bs, Hq, Hkv, D) for _ in range(2)]
+
+    def rows(*shape):
+        return [torch.randn(shape, generator=gen).half() for _ in refs]
+
+    for ref, k, v in zip(refs, rows(21, Hkv, D), rows(21, Hkv, D)):
+        ref.step([21, 0, 0, 0], np.zeros(S, bool), k, v)
+        ref.pool.fork(ref.tables[0], 21, ref.tables[1])
+        ref.ctx[1] = 21
+    sv = ServingStep(S, MB, NB, bs, Hq, Hkv, D, T, dtype=torch.float16, num_layers=2,
+                     pool=pa.DevicePool(NB, bs, pa.PA_POOL_FIFO, host_pool=refs[0].pool))
+    sv.block_tables.copy_(torch.from_numpy(refs[0].tables))
+    sv.context_lens.copy_(torch.from_numpy(refs[0].ctx))
+    for i, ref in enumerate(refs):
+        for got, x in zip(sv.cache(i), ref.codes + ref.scales):
+            got.copy_(torch.from_numpy(x))
+    for new in ([1, 1, 30, 0], [1, 0, 1, 5], [2, 14, 0, 1]):
+        k, v, q = rows(T, Hkv, D), rows(T, Hkv, D), rows(S, Hq, D)
+        sv.schedule(dev(new), dev(np.zeros(S)))
+        outs = [sv.attend(k[i].cuda(), v[i].cuda(), q[i].cuda(), layer=i).clone() for i in range(2)]
+        torch.cuda.synchronize()
+        for i, ref in enumerate(refs):
+            ref.step(new, np.zeros(S, bool), k[i], v[i])
+            assert np.array_equal(sv.block_tables.cpu().numpy(), ref.tables)
+            for got, want in zip(sv.cache(i), ref.codes + ref.scales):
+                assert np.array_equal(got.cpu().numpy(), want)
+            ref.check_out(outs[i], q[i], sv.scale)
+    assert pa.pa_read_device_errors() == 0
+    with pytest.raises(ValueError, match="attend for each"):
+        sv.step(dev([0] * S), dev([0] * S), k[0].cuda(), v[0].cuda(), q[0].cuda())
