@@ -28,6 +28,7 @@ k_scale/v_scale [num_blocks, num_kv_heads, block_size] float32, or
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional, Tuple
 
@@ -35,11 +36,11 @@ import numpy as np
 import torch
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "libpa_b200.so")
+CALL_PATH = os.path.join(os.path.dirname(LIB_PATH), "pa_call.so")
 
 PA_F32, PA_F16, PA_BF16 = 0, 1, 2
 _DT = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}
 
-PA_ERR_WORKSPACE = -9
 PA_DEVERR_BLOCK_ID = 0x1
 PA_DEVERR_SLOT = 0x2
 PA_DEVERR_CONTEXT = 0x4
@@ -170,6 +171,25 @@ class _Library:
 _lib = _Library()
 
 
+class _Binding:
+    """Loads lib/pa_call.so at the first call: the serving step's calls, which
+    check their tensors themselves (contiguous, of the type, on the current
+    device, whose current stream is used unless one is given; else ValueError)."""
+
+    def __getattr__(self, name):
+        if not os.path.exists(CALL_PATH):
+            raise ImportError(f"{CALL_PATH} is not built; run `python -m paged_kv_cache_340_b200._build`")
+        spec = importlib.util.spec_from_file_location("pa_call", CALL_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        for fn in ("dpool_append", "dpool_release", "append_q8b", "decode_q8b", "copy_blocks_q8b"):
+            setattr(self, fn, getattr(module, fn))  # found without this call from now on
+        return getattr(module, name)
+
+
+_call = _Binding()
+
+
 def status_string(status: int) -> str:
     return _lib.pa_status_string(int(status)).decode()
 
@@ -189,19 +209,10 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return t.data_ptr()
 
 
-def _addr(t: torch.Tensor, dtype: torch.dtype, device: int) -> int:
-    """Address of a contiguous tensor of the type on the device (the current
-    one: its stream is the call's)."""
-    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
-        raise ValueError(f"expected a contiguous {dtype} tensor on cuda:{device}, got {t.dtype} on {t.device} "
-                         f"of shape {tuple(t.shape)} and strides {t.stride()}")
-    return t.data_ptr()
-
-
-def _stream(stream, device: int = -1) -> Optional[int]:
+def _stream(stream) -> Optional[int]:
     if stream is None:
         # torch.cuda.current_stream().cuda_stream without the Stream object (0.3 us instead of 3.3)
-        return torch._C._cuda_getCurrentRawStream(device if device >= 0 else torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -476,15 +487,8 @@ def pa_dpool_append(pool: DevicePool, block_tables, context_lens, new_lens, q_st
     length in block_tables [S, MB] and context_lens [S], q_start [S + 1],
     slots in slot_mapping [max_tokens] (then -1), pairs to copy in cow_pairs
     [S, 2] int64 and their number in num_cow [1] (all on the device; see pa.h)."""
-    S, MB = block_tables.shape
-    if context_lens.shape != (S,) or new_lens.shape != (S,) or q_start.shape != (S + 1,) or cow_pairs.shape != (S, 2):
-        raise ValueError("pa_dpool_append: one row, length and pair per sequence, and one more q_start")
-    dev, i32 = torch.cuda.current_device(), torch.int32
-    rc = _lib.pa_dpool_append(_addr(pool.state, i32, dev), pool.num_blocks, pool.block_size,
-                              _addr(block_tables, i32, dev), MB, _addr(context_lens, i32, dev),
-                              _addr(new_lens, i32, dev), S, _addr(q_start, i32, dev), _addr(slot_mapping, i32, dev),
-                              slot_mapping.shape[0], _addr(cow_pairs, torch.int64, dev), _addr(num_cow, i32, dev),
-                              _stream(stream, dev))
+    rc = _call.dpool_append(pool.state, pool.num_blocks, pool.block_size, block_tables, context_lens, new_lens, q_start,
+                            slot_mapping, cow_pairs, num_cow, stream)
     if rc:
         _check(rc, "pa_dpool_append")
 
@@ -492,13 +496,7 @@ def pa_dpool_append(pool: DevicePool, block_tables, context_lens, new_lens, q_st
 def pa_dpool_release(pool: DevicePool, block_tables, context_lens, finished, stream=None) -> None:
     """Returns the blocks of every sequence s with finished[s] != 0 (device
     int32 [S]); its table entries become -1 and its length 0."""
-    S, MB = block_tables.shape
-    if context_lens.shape != (S,) or finished.shape != (S,):
-        raise ValueError("pa_dpool_release: one row, length and mark per sequence")
-    dev, i32 = torch.cuda.current_device(), torch.int32
-    rc = _lib.pa_dpool_release(_addr(pool.state, i32, dev), pool.num_blocks, pool.block_size,
-                               _addr(block_tables, i32, dev), MB, _addr(context_lens, i32, dev),
-                               _addr(finished, i32, dev), S, _stream(stream, dev))
+    rc = _call.dpool_release(pool.state, pool.num_blocks, pool.block_size, block_tables, context_lens, finished, stream)
     if rc:
         _check(rc, "pa_dpool_release")
 
@@ -506,30 +504,11 @@ def pa_dpool_release(pool: DevicePool, block_tables, context_lens, finished, str
 # ------------------------------------- int8 caches with a scale per block
 # k_cache/v_cache int8 [NB, Hkv, bs, D]; k_scale/v_scale float32 [NB, Hkv].
 
-def _q8b_cache(k_cache, v_cache, k_scale, v_scale):
-    shape = k_cache.shape
-    NB, Hkv, _, _ = shape
-    if v_cache.shape != shape or k_scale.shape != (NB, Hkv) or v_scale.shape != (NB, Hkv):
-        raise ValueError("expected k_cache and v_cache [NB, Hkv, bs, D] with k_scale and v_scale [NB, Hkv]")
-    return shape
-
-
 def pa_append_q8b(key, value, q_start, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                   stream=None) -> None:
     """Writes rows q_start[s] .. q_start[s+1]-1 of key and value [T, Hkv, D] as
     the last tokens of sequence s, quantized with one scale per (block, head)."""
-    NB, Hkv, bs, D = _q8b_cache(k_cache, v_cache, k_scale, v_scale)
-    T = key.shape[0]
-    S, MB = block_tables.shape
-    if key.shape != (T, Hkv, D) or value.shape != (T, Hkv, D):
-        raise ValueError("pa_append_q8b: key and value are [T, Hkv, D]")
-    if q_start.shape != (S + 1,) or context_lens.shape != (S,):
-        raise ValueError("pa_append_q8b: one table row and length per sequence, and one more q_start")
-    dev, i8, i32, f32, src = torch.cuda.current_device(), torch.int8, torch.int32, torch.float32, key.dtype
-    rc = _lib.pa_append_q8b(_addr(key, src, dev), _addr(value, src, dev), _dtype(key), _addr(q_start, i32, dev), T,
-                            _addr(k_cache, i8, dev), _addr(v_cache, i8, dev), _addr(k_scale, f32, dev),
-                            _addr(v_scale, f32, dev), _addr(block_tables, i32, dev), MB,
-                            _addr(context_lens, i32, dev), S, NB, Hkv, D, bs, _stream(stream, dev))
+    rc = _call.append_q8b(key, value, q_start, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, stream)
     if rc:
         _check(rc, "pa_append_q8b")
 
@@ -543,27 +522,8 @@ def pa_decode_q8b(out, query, k_cache, v_cache, k_scale, v_scale, block_tables, 
     """Decode over a cache with a scale per (block, head). max_context_len
     bounds context_lens; with a workspace few, long sequences are split along
     their tokens."""
-    NB, Hkv, bs, Dk = _q8b_cache(k_cache, v_cache, k_scale, v_scale)
-    S, Hq, D = query.shape
-    MB = block_tables.shape[1]
-    if Dk != D or out.shape != (S, Hq, D) or context_lens.shape != (S,) or block_tables.shape != (S, MB):
-        raise ValueError("pa_decode_q8b: query and out [S, Hq, D], one table row and length per sequence")
-    dev, i8, i32, f32 = torch.cuda.current_device(), torch.int8, torch.int32, torch.float32
-    ws = order = None
-    nbytes = 0
-    if workspace is not None:
-        ws, nbytes = _addr(workspace, workspace.dtype, dev), workspace.nbytes
-        if nbytes == 0:
-            _check(PA_ERR_WORKSPACE, "pa_decode_q8b")  # an empty tensor has no address: not "no workspace"
-    if seq_order is not None:
-        if seq_order.shape != (S,):
-            raise ValueError("pa_decode_q8b: seq_order has one entry per sequence")
-        order = _addr(seq_order, i32, dev)
-    rc = _lib.pa_decode_q8b(_addr(out, out.dtype, dev), _addr(query, query.dtype, dev), _dtype(query),
-                            _addr(k_cache, i8, dev), _addr(v_cache, i8, dev), _addr(k_scale, f32, dev),
-                            _addr(v_scale, f32, dev), _addr(block_tables, i32, dev), MB,
-                            _addr(context_lens, i32, dev), S, Hq, Hkv, D, scale, bs, NB, max_context_len, _dtype(out),
-                            order, ws, nbytes, _stream(stream, dev))
+    rc = _call.decode_q8b(out, query, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
+                          max_context_len, workspace, seq_order, stream)
     if rc:
         _check(rc, "pa_decode_q8b")
 
@@ -573,7 +533,9 @@ def pa_decode_q8b_withhold_tile(out, query, k_cache, v_cache, k_scale, v_scale, 
     """pa_decode_q8b with the copy of one 128-token K tile of one (sequence, kv
     head) withheld, so that its bounded waits run out (a test of the timeout
     path; that head's output is undefined)."""
-    NB, Hkv, bs, _ = _q8b_cache(k_cache, v_cache, k_scale, v_scale)
+    NB, Hkv, bs, _ = k_cache.shape
+    if v_cache.shape != k_cache.shape or k_scale.shape != (NB, Hkv) or v_scale.shape != (NB, Hkv):
+        raise ValueError("expected k_cache and v_cache [NB, Hkv, bs, D] with k_scale and v_scale [NB, Hkv]")
     S, Hq, D = query.shape
     rc = _lib.pa_decode_q8b_withhold_tile(_ptr(out), _ptr(query), _dtype(query), _ptr(k_cache), _ptr(v_cache),
                                           _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1],
@@ -586,15 +548,7 @@ def pa_decode_q8b_withhold_tile(out, query, k_cache, v_cache, k_scale, v_scale, 
 def pa_copy_blocks_q8b(k_cache, v_cache, k_scale, v_scale, src_dst_pairs, num_pairs=None, stream=None) -> None:
     """pa_copy_blocks of codes and scales; with num_pairs (a device int32) only
     that many of the pairs."""
-    NB, Hkv, bs, D = _q8b_cache(k_cache, v_cache, k_scale, v_scale)
-    n = src_dst_pairs.shape[0]
-    if src_dst_pairs.shape != (n, 2):
-        raise ValueError("pa_copy_blocks_q8b: src_dst_pairs is [n, 2]")
-    dev, i8, f32 = torch.cuda.current_device(), torch.int8, torch.float32
-    rc = _lib.pa_copy_blocks_q8b(_addr(k_cache, i8, dev), _addr(v_cache, i8, dev), _addr(k_scale, f32, dev),
-                                 _addr(v_scale, f32, dev), _addr(src_dst_pairs, torch.int64, dev),
-                                 None if num_pairs is None else _addr(num_pairs, torch.int32, dev), n, NB, Hkv, D, bs,
-                                 _stream(stream, dev))
+    rc = _call.copy_blocks_q8b(k_cache, v_cache, k_scale, v_scale, src_dst_pairs, num_pairs, stream)
     if rc:
         _check(rc, "pa_copy_blocks_q8b")
 

@@ -2,7 +2,9 @@
 
 Every translation unit is compiled for sm_100a only
 (``-gencode arch=compute_100a,code=sm_100a``), in parallel, then linked into
-one shared library. Run ``python -m paged_kv_cache_340_b200._build``.
+one shared library. The binding of the serving step's calls
+(binding/pa_call.cpp, the only part that knows torch) becomes a Python module
+beside it, lib/pa_call.so. Run ``python -m paged_kv_cache_340_b200._build``.
 """
 from __future__ import annotations
 
@@ -11,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(PKG, "lib")
 OBJDIR = os.path.join(ROOT, "_build", "obj")
 LIB = os.path.join(LIBDIR, "libpa_b200.so")
+BINDING = os.path.join(PKG, "binding", "pa_call.cpp")
+BINDING_LIB = os.path.join(LIBDIR, "pa_call.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++20", "-lineinfo", "-Xcompiler", "-fPIC,-O3", "-I" + INCLUDE, "-I" + CSRC,
@@ -81,6 +86,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs)
         os.replace(tmp, LIB)
+    if force or _stale(BINDING_LIB, [BINDING, os.path.join(INCLUDE, "pa.h")]):
+        import torch
+        home = os.path.dirname(torch.__file__)
+        cuda_inc = os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")
+        tmp = BINDING_LIB + f".tmp{os.getpid()}"
+        run(["g++", "-O2", "-std=c++20", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+             "-I" + INCLUDE, "-I" + os.path.join(home, "include"), "-I" + sysconfig.get_paths()["include"], "-I" + cuda_inc,
+             BINDING, "-o", tmp, "-L" + os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+             "-L" + LIBDIR, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"])
+        os.replace(tmp, BINDING_LIB)
     return LIB
 
 
