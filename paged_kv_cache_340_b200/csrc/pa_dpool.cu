@@ -38,7 +38,8 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 // CTAs of the cluster: 8 is the largest portable size; where a call may have
-// enough to do for more, 16.
+// enough to do for more, 16; one where that is enough, since every barrier and
+// phase then stays within an SM.
 constexpr int kCluster = 8, kClusterLarge = 16;
 constexpr int kBatch = 8;    // items of a warp whose accesses are in flight at once
 constexpr int kClaimed = INT32_MIN;  // the count of a block that release_kernel is freeing
@@ -172,11 +173,23 @@ template <int kPer> __global__ void __launch_bounds__(kThreads, 1) append_kernel
     int *take_pre = tok_pre + S + 1;     // [S + 1] blocks taken before sequence s
     int *ctx_cow = take_pre + S + 1;     // [S] context length, sign bit: its last block is copied
     __shared__ long long sums[2 * (kWarps + 1)];
+    // The writers of shared blocks are counted in a hash table of each CTA (every
+    // CTA goes over every sequence), or in the pool's scratch where the sequences
+    // are too many for one: a barrier of the cluster and two trips to L2 more (64
+    // single tokens 8.1 us that way, 7.8 with the table; 1000 sequences 10.6, 10.0).
+    constexpr bool kLocal = kPer == 1;
+    constexpr int kHash = kLocal ? 2 * kThreads : 1;
+    __shared__ int h_block[kHash], h_writers[kHash], h_last[kHash];
 
     wait_previous();
     allow_next();
     const Pool p = views(q.state, nb);
     const Header hdr(p);
+    if constexpr (kLocal)
+        for (int i = tid; i < kHash; i += kThreads) {
+            h_block[i] = h_last[i] = -1;
+            h_writers[i] = 0;
+        }
     const int per = (S + kThreads - 1) / kThreads;
     const int s0 = tid * per, s1 = min(S, s0 + per);
     int ctx[kPer], nw[kPer], blk[kPer], ref[kPer];
@@ -227,12 +240,27 @@ template <int kPer> __global__ void __launch_bounds__(kThreads, 1) append_kernel
         if (ref[i] < 1) bad |= PA_DEVERR_POOL;
         if (ref[i] <= 1) {
             blk[i] = -1;  // this sequence's alone: written in place
-        } else if (mine) {
+        } else if (!kLocal && mine) {
             atomicAdd(p.writers + blk[i], 1);
             atomicMax(p.last_writer + blk[i], s0 + i);
         }
     }
-    cluster.sync();
+    int place = 0;  // of this thread's block in the table
+    if constexpr (kLocal) {
+        __syncthreads();
+        if (blk[0] >= 0) {
+            place = (int)((unsigned)blk[0] * 2654435769u >> 16) & (kHash - 1);
+            for (;; place = (place + 1) & (kHash - 1)) {  // at most half of the places are taken
+                const int held = atomicCAS(h_block + place, -1, blk[0]);
+                if (held == -1 || held == blk[0]) break;
+            }
+            atomicAdd(h_writers + place, 1);
+            atomicMax(h_last + place, s0);
+        }
+        __syncthreads();
+    } else {
+        cluster.sync();
+    }
 
     // ---- takes and their places; the same in every CTA
     long long tok_at = 0;
@@ -242,7 +270,8 @@ template <int kPer> __global__ void __launch_bounds__(kThreads, 1) append_kernel
     for (int i = 0; i < kPer; ++i) {
         cow[i] = false;
         if (blk[i] >= 0) {
-            const int w = __ldcg(p.writers + blk[i]), last = __ldcg(p.last_writer + blk[i]);
+            const int w = kLocal ? h_writers[place] : __ldcg(p.writers + blk[i]);
+            const int last = kLocal ? h_last[place] : __ldcg(p.last_writer + blk[i]);
             if (w > ref[i]) bad |= PA_DEVERR_POOL;  // more tables hold the block than its count says
             cow[i] = !(w == ref[i] && last == s0 + i);
         }
@@ -279,7 +308,7 @@ template <int kPer> __global__ void __launch_bounds__(kThreads, 1) append_kernel
 
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-        if (mine && blk[i] >= 0) {
+        if (!kLocal && mine && blk[i] >= 0) {
             p.writers[blk[i]] = 0;
             p.last_writer[blk[i]] = -1;
         }
@@ -618,15 +647,14 @@ struct KernelCache {
     AttrCache smem, large;
 };
 
-// Launches one cluster; `large`: of kClusterLarge CTAs, where the device can hold one.
+// Launches one cluster of `ctas` CTAs (kClusterLarge where the device can hold one, else kCluster).
 template <typename P>
-static cudaError_t launch_cluster(void (*kern)(P), const P &q, int smem, KernelCache *cache, int smem_max, bool large,
-                                  cudaStream_t stream) {
+static cudaError_t launch_cluster(void (*kern)(P), const P &q, int smem, KernelCache *cache, int smem_max,
+                                  unsigned ctas, cudaStream_t stream) {
     const void *fn = reinterpret_cast<const void *>(kern);
     cudaError_t e = ensure_smem_attr(fn, smem_max, &cache->smem);
     if (e != cudaSuccess) return e;
-    unsigned ctas = kCluster;
-    if (large) {
+    if (ctas == kClusterLarge) {
         int dev = 0;
         e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
@@ -652,7 +680,7 @@ static cudaError_t launch_cluster(void (*kern)(P), const P &q, int smem, KernelC
             if (fits) cache->large.ctx[dev].store(current_context(), std::memory_order_release);
             else (void)cudaGetLastError();
         }
-        if (fits) ctas = kClusterLarge;
+        if (!fits) ctas = kCluster;
     }
     return launch_after(kern, dim3(ctas), kThreads, (size_t)smem, ctas, stream, q);
 }
@@ -705,14 +733,18 @@ extern "C" int pa_dpool_append(void *state, int num_blocks, int block_size, int3
     q.num_blocks = num_blocks;
     q.block_size = block_size;
     const int smem = (3 * num_seqs + 2) * 4;
-    const bool large = max_tokens > 65536;  // over two rounds of four slots for every thread of 8 CTAs
+    // One CTA: a round of four slots for every thread (64 single tokens 7.8 -> 7.2 us, 296 short ones
+    // 8.7 -> 8.2). 16: over two rounds for every thread of 8.
+    const unsigned ctas = num_seqs <= dpool::kThreads && max_tokens <= 4 * dpool::kThreads ? 1
+                          : max_tokens > 65536                                            ? dpool::kClusterLarge
+                                                                                          : dpool::kCluster;
     static dpool::KernelCache one, most;
     cudaError_t e =
         num_seqs <= dpool::kThreads
-            ? dpool::launch_cluster(dpool::append_kernel<1>, q, smem, &one, (3 * dpool::kThreads + 2) * 4, large,
+            ? dpool::launch_cluster(dpool::append_kernel<1>, q, smem, &one, (3 * dpool::kThreads + 2) * 4, ctas,
                                     stream)
             : dpool::launch_cluster(dpool::append_kernel<dpool::kPerMost>, q, smem, &most,
-                                    (3 * PA_DPOOL_MAX_SEQS + 2) * 4, large, stream);
+                                    (3 * PA_DPOOL_MAX_SEQS + 2) * 4, ctas, stream);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -737,14 +769,19 @@ extern "C" int pa_dpool_release(void *state, int num_blocks, int block_size, int
     q.num_blocks = num_blocks;
     q.block_size = block_size;
     const int smem = (2 * num_seqs + 1) * 4;
-    // more table entries than the warps of 8 CTAs hold at once
-    const bool large = (long long)num_seqs * max_blocks_per_seq > 32ll * dpool::kBatch * dpool::kWarps * dpool::kCluster;
+    // Items that the warps of a CTA hold at once. One CTA: no more of them (168 sequences 8.6 -> 7.2 us; two
+    // batches took 9.7 -> 11.1 us for 560, four 11.0 -> 29.7 for 858). 16: more than 8 CTAs hold.
+    constexpr long long kHeld = dpool::kBatch * dpool::kWarps;
+    const long long most_items = (long long)num_seqs * ((max_blocks_per_seq + 31ll) / 32);
+    const unsigned ctas = most_items <= kHeld ? 1
+                          : (long long)num_seqs * max_blocks_per_seq > 32 * kHeld * dpool::kCluster ? dpool::kClusterLarge
+                                                                                                    : dpool::kCluster;
     static dpool::KernelCache one, most;
     cudaError_t e =
         num_seqs <= dpool::kThreads
-            ? dpool::launch_cluster(dpool::release_kernel<1>, q, smem, &one, (2 * dpool::kThreads + 1) * 4, large,
+            ? dpool::launch_cluster(dpool::release_kernel<1>, q, smem, &one, (2 * dpool::kThreads + 1) * 4, ctas,
                                     stream)
             : dpool::launch_cluster(dpool::release_kernel<dpool::kPerMost>, q, smem, &most,
-                                    (2 * PA_DPOOL_MAX_SEQS + 1) * 4, large, stream);
+                                    (2 * PA_DPOOL_MAX_SEQS + 1) * 4, ctas, stream);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
