@@ -261,3 +261,64 @@ def test_release_of_many_entries(pa):
     b.release(rng.random(S) < 0.5)
     b.release(np.ones(S, int))
     assert b.host.num_free() == 130000
+
+
+@pytest.mark.parametrize("S,pad", [(1000, 0), (1000, 9000), (1024, 5), (1025, 5)])
+def test_shared_blocks_of_many_writers(pa, S, pad):
+    """Every sequence is a fork of some other, in groups of one to nine; all of
+    a group write into its last block, or all but some. Few slots and many,
+    and on both sides of where a thread holds one sequence."""
+    rng = np.random.default_rng(S + pad)
+    forks, at = [], 0
+    while at < S:
+        n = int(rng.integers(1, 10))
+        forks += [(at, j, 5 + at % 40) for j in range(at + 1, min(S, at + n))]
+        at += n
+    b = Both(pa, S, 8, 9 * S, 16, pa.PA_POOL_FIFO, 16, forks)
+    b.append((rng.random(S) < 0.9).astype(int), pad=pad)
+    b.append(rng.integers(0, 4, S), pad=pad)
+    b.release(rng.random(S) < 0.5)
+    b.append(rng.integers(0, 20, S), pad=pad)
+
+
+@pytest.mark.parametrize("S,MB", [(5, 6), (400, 6)])
+def test_release_of_a_block_listed_twice_or_free_changes_nothing(pa, S, MB):
+    """Blocks of one holder each, so that each is claimed at once: one that a
+    second entry lists too, and one that is free already."""
+    b = Both(pa, S, MB, 3 * S + 5, 16, pa.PA_POOL_LIFO, 17)
+    b.append(np.full(S, 33))
+    keep = int(b.d_tables[S - 2, 1])
+    for value in (int(b.d_tables[0, 2]), b.pool.free_list()[1]):
+        b.d_tables[S - 2, 1] = value
+        before = [t.clone() for t in (b.pool.state, b.d_tables, b.d_ctx)]
+        pa.pa_dpool_release(b.pool, b.d_tables, b.d_ctx, torch.ones(S, dtype=torch.int32, device="cuda"))
+        assert pa.pa_read_device_errors() == 0x20
+        for t, w in zip((b.pool.state, b.d_tables, b.d_ctx), before):
+            assert torch.equal(t, w)
+    b.d_tables[S - 2, 1] = keep
+    b.release(np.ones(S, int))
+
+
+def test_binding_refuses_wrong_types_and_shapes(pa):
+    b = Both(pa, 3, 4, 20, 16, pa.PA_POOL_FIFO, 18)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    good = [b.d_tables, b.d_ctx, torch.ones(3, **i32), torch.empty(4, **i32), torch.empty(9, **i32),
+            torch.empty((3, 2), dtype=torch.int64, device="cuda"), torch.empty(1, **i32)]
+    before = [t.clone() for t in (b.pool.state, b.d_tables, b.d_ctx)]
+    for i, bad in ((0, b.d_tables.t()), (0, b.d_ctx), (1, b.d_ctx[:2]), (1, b.d_ctx.long()), (2, torch.ones(3, dtype=torch.int32)),
+                   (3, torch.empty(3, **i32)), (4, torch.empty((3, 3), **i32)), (4, torch.empty(18, **i32)[::2]),
+                   (5, torch.empty((3, 2), **i32)), (5, torch.empty((2, 2), dtype=torch.int64, device="cuda")),
+                   (6, torch.empty(0, **i32))):
+        args = list(good)
+        args[i] = bad
+        with pytest.raises(ValueError):
+            pa.pa_dpool_append(b.pool, *args)
+    with pytest.raises(TypeError):
+        pa.pa_dpool_append(b.pool, *good[:2], [1, 1, 1], *good[3:])
+    with pytest.raises(ValueError):
+        pa.pa_dpool_release(b.pool, b.d_tables, b.d_ctx, torch.ones(3, dtype=torch.bool, device="cuda"))
+    with pytest.raises(AttributeError):
+        pa.pa_dpool_append(b.pool, *good, stream="0")
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, w) for t, w in zip((b.pool.state, b.d_tables, b.d_ctx), before))
+    assert pa.pa_read_device_errors() == 0

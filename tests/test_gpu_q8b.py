@@ -563,3 +563,57 @@ def test_binding_refuses_wrong_types_and_shapes(pa):
     with pytest.raises(ValueError):
         pa.pa_append_q8b(q[:, :2], q[:, :2].float(), torch.tensor([0, 1], dtype=torch.int32, device="cuda"), *d)
     assert pa.pa_read_device_errors() == 0
+
+
+def test_stream_as_object_handle_or_current(pa):
+    """The three ways to give a stream, each behind work of that stream that the call has to wait for."""
+    c = Case(4, 2, 128, 16, [70, 33], seed=39)
+    d = [torch.from_numpy(a).cuda() for a in (c.kq, c.vq, c.ks, c.vs, c.tables, c.ctx)]
+    q = c.q.half().cuda()
+    want = torch.empty_like(q)
+    pa.pa_decode_q8b(want, q, *d, c.scale, 70)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    for give in (st, st.cuda_stream, None):
+        late, out, nxt = torch.zeros_like(q), torch.zeros_like(q), torch.zeros_like(q)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            torch.cuda._sleep(2_000_000)
+            late.copy_(q)
+            if give is None:
+                pa.pa_decode_q8b(out, late, *d, c.scale, 70)
+        if give is not None:
+            pa.pa_decode_q8b(out, late, *d, c.scale, 70, stream=give)
+        with torch.cuda.stream(st):
+            nxt.copy_(out)
+        torch.cuda.synchronize()
+        assert torch.equal(nxt, want)
+    assert pa.pa_read_device_errors() == 0
+
+
+def test_binding_takes_numpy_numbers_and_refuses_the_rest(pa):
+    c = Case(4, 2, 128, 16, [20], seed=40)
+    d = [torch.from_numpy(a).cuda() for a in (c.kq, c.vq, c.ks, c.vs, c.tables, c.ctx)]
+    q = c.q.half().cuda()
+    out = torch.empty_like(q)
+    pa.pa_decode_q8b(out, q, *d, np.float32(c.scale), np.int64(20))
+    c.check(out, torch.float16)
+    with pytest.raises(OverflowError):
+        pa.pa_decode_q8b(out, q, *d, c.scale, 1 << 40)
+    with pytest.raises(TypeError):
+        pa.pa_decode_q8b(out, q, *d, c.scale, 20.5)
+    with pytest.raises(TypeError):
+        pa.pa_decode_q8b(out, q, *d, None, 20)
+    with pytest.raises(TypeError):
+        pa.pa_decode_q8b(out, q.cpu().numpy(), *d, c.scale, 20)
+    with pytest.raises(ValueError):
+        pa.pa_decode_q8b(out, q.cpu(), *d, c.scale, 20)
+    with pytest.raises(ValueError):
+        pa.pa_decode_q8b(out, q.to(torch.int16), *d, c.scale, 20)
+    with pytest.raises(ValueError):
+        pa.pa_copy_blocks_q8b(*d[:4], torch.zeros((1, 3), dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError):
+        pa.pa_copy_blocks_q8b(*d[:4], torch.zeros((1, 2), dtype=torch.int64, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda"))
+    with pytest.raises(pa.PagedAttentionError):
+        pa.pa_decode_q8b(out, q, *d, float("nan"), 20)
+    assert pa.pa_read_device_errors() == 0
