@@ -678,9 +678,9 @@ int pa_append_q8b(const void *key, const void *value, pa_dtype src_dtype, const 
  * query is q_dtype (PA_F16 or PA_BF16); out_dtype q_dtype or PA_F32.
  * max_context_len (at most 2^30) bounds every context_lens[s] (longer ones are
  * clamped, PA_DEVERR_CONTEXT); the closer the bound, the better the split.
- * A query row that is not finite gives a NaN output row. workspace (nullable device buffer, 16-byte aligned, of
- * at least pa_decode_q8b_workspace_bytes, else PA_ERR_WORKSPACE) lets a batch
- * of few, long sequences be split along the tokens over more CTAs and joined;
+ * A query row that is not finite gives a NaN output row. workspace (nullable
+ * device buffer, 16-byte aligned, of at least pa_decode_q8b_workspace_bytes,
+ * else PA_ERR_WORKSPACE) lets a batch of few, long sequences be split along the tokens over more CTAs and joined;
  * without it each (sequence, kv head) is one CTA's work. Its contents need no
  * initialisation and mean nothing after the call; calls that may run at the
  * same time must not share one. Other arguments, checks and device errors as
