@@ -680,11 +680,11 @@ int pa_append_q8b(const void *key, const void *value, pa_dtype src_dtype, const 
  * clamped, PA_DEVERR_CONTEXT); the closer the bound, the better the split.
  * A query row that is not finite gives a NaN output row. workspace (nullable
  * device buffer, 16-byte aligned, of at least pa_decode_q8b_workspace_bytes,
- * else PA_ERR_WORKSPACE) lets a batch of few, long sequences be split along the tokens over more CTAs and joined;
- * without it each (sequence, kv head) is one CTA's work. Its contents need no
- * initialisation and mean nothing after the call; calls that may run at the
- * same time must not share one. Other arguments, checks and device errors as
- * pa_decode.
+ * else PA_ERR_WORKSPACE) lets a batch of few, long sequences be split along
+ * the tokens over more CTAs and joined; without it each (sequence, kv head) is
+ * one CTA's work. Its contents need no initialisation and mean nothing after
+ * the call; calls that may run at the same time must not share one. Other
+ * arguments, checks and device errors as pa_decode.
  */
 size_t pa_decode_q8b_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                                      int max_context_len);
