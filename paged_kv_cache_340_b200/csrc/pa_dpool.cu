@@ -78,7 +78,20 @@ struct ReleaseParams {
     unsigned int *err;
 };
 
-__device__ __forceinline__ int ceil_div(int a, int b) { return a / b + (a % b != 0); }
+// Quotients by the block size of numbers from 0 on; a power of two is a shift, a
+// division some 25 instructions.
+struct ByBlock {
+    int bs, shift;  // (-1: no power of two)
+    __device__ __forceinline__ explicit ByBlock(int size) {
+        bs = size;
+        shift = (size & (size - 1)) == 0 ? 31 - __clz(size) : -1;
+    }
+    __device__ __forceinline__ int down(int x) const { return shift >= 0 ? x >> shift : x / bs; }
+    __device__ __forceinline__ int up(int x) const {
+        const int n = down(x);
+        return n + (n * bs != x);
+    }
+};
 
 struct Header {
     int nb, bs, policy, head, count, magic;
@@ -163,6 +176,7 @@ template <int kPer> __global__ void __launch_bounds__(kThreads, 1) append_kernel
     const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
     const int tid = threadIdx.x;
     const int S = q.num_seqs, MB = q.max_blocks, nb = q.num_blocks, bs = q.block_size;
+    const ByBlock by(bs);
     // every CTA works out every sequence; the ones a CTA's output threads
     // answer for (marks, per-sequence outputs) are those of its slice
     const bool mine = tid / (kThreads / ctas) == rank;
@@ -225,8 +239,8 @@ template <int kPer> __global__ void __launch_bounds__(kThreads, 1) append_kernel
         } else if ((long long)ctx[i] + nw[i] > (long long)MB * bs) {
             bad |= PA_DEVERR_POOL;
             ctx[i] = nw[i] = 0;
-        } else if (nw[i] > 0 && ctx[i] % bs != 0) {
-            blk[i] = __ldcg(q.tables + (size_t)(s0 + i) * MB + ctx[i] / bs);
+        } else if (nw[i] > 0 && by.down(ctx[i]) * bs != ctx[i]) {
+            blk[i] = __ldcg(q.tables + (size_t)(s0 + i) * MB + by.down(ctx[i]));
             if (blk[i] < 0 || blk[i] >= nb) {
                 bad |= PA_DEVERR_BLOCK_ID;
                 blk[i] = -1;
@@ -276,7 +290,7 @@ template <int kPer> __global__ void __launch_bounds__(kThreads, 1) append_kernel
             cow[i] = !(w == ref[i] && last == s0 + i);
         }
         tok_at += nw[i];
-        takes += (int)cow[i] + ceil_div(ctx[i] + nw[i], bs) - ceil_div(ctx[i], bs);
+        takes += (int)cow[i] + by.up(ctx[i] + nw[i]) - by.up(ctx[i]);
         cows += cow[i];
     }
     // takes and cows are below 2^30 (sequences x table entries): one 64-bit scan for both
@@ -297,7 +311,7 @@ template <int kPer> __global__ void __launch_bounds__(kThreads, 1) append_kernel
             take_pre[s] = k;
             ctx_cow[s] = cow[i] ? (ctx[i] | (int)0x80000000) : ctx[i];
             t += nw[i];
-            k += (int)cow[i] + ceil_div(ctx[i] + nw[i], bs) - ceil_div(ctx[i], bs);
+            k += (int)cow[i] + by.up(ctx[i] + nw[i]) - by.up(ctx[i]);
         }
         if (tid == 0) {
             tok_pre[S] = (int)all_tok;
@@ -337,7 +351,7 @@ template <int kPer> __global__ void __launch_bounds__(kThreads, 1) append_kernel
                 ++cow_at;
             }
             t += nw[i];
-            k += (int)cow[i] + ceil_div(ctx[i] + nw[i], bs) - ceil_div(ctx[i], bs);
+            k += (int)cow[i] + by.up(ctx[i] + nw[i]) - by.up(ctx[i]);
         }
     }
     for (int i = all_cows + gtid; i < S; i += gstep)
@@ -347,7 +361,7 @@ template <int kPer> __global__ void __launch_bounds__(kThreads, 1) append_kernel
         const int c = ctx_cow[s] & 0x7fffffff, cw = ctx_cow[s] < 0;
         const int id = block_of(k);
         // the copy of the last block (if any) is the sequence's first take
-        const int j = k - take_pre[s] < cw ? c / bs : ceil_div(c, bs) + k - take_pre[s] - cw;
+        const int j = k - take_pre[s] < cw ? by.down(c) : by.up(c) + k - take_pre[s] - cw;
         q.tables[(size_t)s * MB + j] = id;
         p.ref[id] = 1;
     }
@@ -372,7 +386,7 @@ template <int kPer> __global__ void __launch_bounds__(kThreads, 1) append_kernel
                     while (t >= tok_pre[s + 1]);
                 next = tok_pre[s + 1];
                 const int pos = (ctx_cow[s] & 0x7fffffff) + t - tok_pre[s];
-                j = pos / bs;
+                j = by.down(pos);
                 o = pos - j * bs;
             } else if (++o == bs) {
                 o = 0;
@@ -382,7 +396,7 @@ template <int kPer> __global__ void __launch_bounds__(kThreads, 1) append_kernel
             }
             if (look) {
                 const int c = ctx_cow[s] & 0x7fffffff, cw = ctx_cow[s] < 0;
-                const int have = ceil_div(c, bs);
+                const int have = by.up(c);
                 if (j >= have) id = block_of(take_pre[s] + cw + j - have);
                 else if (cw) id = block_of(take_pre[s]);
                 else id = __ldcg(q.tables + (size_t)s * MB + j);  // kept: no thread writes this entry
@@ -412,6 +426,7 @@ template <int kPer> __global__ void __launch_bounds__(kThreads, 1) release_kerne
     const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = q.num_seqs, MB = q.max_blocks, nb = q.num_blocks, bs = q.block_size;
+    const ByBlock by(bs);
 
     extern __shared__ int dyn[];
     int *item_pre = dyn;             // [S + 1] 32-entry items before sequence s
@@ -453,7 +468,7 @@ template <int kPer> __global__ void __launch_bounds__(kThreads, 1) release_kerne
             bad |= PA_DEVERR_CONTEXT;
             n[i] = 0;
         }
-        n[i] = ceil_div(n[i], bs);
+        n[i] = by.up(n[i]);
         items += (n[i] + 31) / 32;
     }
     int all_items;
