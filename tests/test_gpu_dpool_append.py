@@ -322,3 +322,14 @@ def test_binding_refuses_wrong_types_and_shapes(pa):
     torch.cuda.synchronize()
     assert all(torch.equal(t, w) for t, w in zip((b.pool.state, b.d_tables, b.d_ctx), before))
     assert pa.pa_read_device_errors() == 0
+
+
+@pytest.mark.parametrize("bs", [1, 3, 24, 48])
+def test_block_sizes_of_every_kind(pa, bs):
+    rng = np.random.default_rng(bs)
+    b = Both(pa, 40, 60, 3000, bs, pa.PA_POOL_FIFO, 19, [(i, i + 1, bs + 1) for i in range(0, 40, 5)])
+    for hi in (1, 2 * bs, 7):
+        b.append(np.minimum(rng.integers(0, hi + 1, 40), 60 * bs - b.ctx), pad=2)
+    b.release(rng.random(40) < 0.5)
+    b.append(np.minimum(rng.integers(0, 20 * bs, 40), 60 * bs - b.ctx))
+    b.release(np.ones(40, int))
