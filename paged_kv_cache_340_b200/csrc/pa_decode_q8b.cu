@@ -457,11 +457,8 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
             int x = blockIdx.x, y = blockIdx.y, z = blockIdx.z;
             bool more = true, sound = true;
             int tiles = 0;  // of all items so far
-            // claims: answers that have come; asked: one more is on its way
-            int claims = 0;
-            bool asked = false;
-            // n: items handed on (a partition past its sequence's end is dropped here)
-            for (int n = 0; sound;) {
+            // n: items handed on (a partition past its sequence's end is dropped here), claims: answers asked for
+            for (int n = 0, claims = 0; sound;) {
                 const int slot = n % kItems;
                 Item &it = items[slot];
                 auto slot_free = [&]() {
@@ -469,6 +466,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                         sound = __all_sync(0xffffffffu, wait(i_empty + slot, (n / kItems - 1) & 1));
                     return sound;
                 };
+                bool asked = false;  // and not answered
                 auto claim = [&]() {  // asks for the next item
                     if (lane == 0) {
                         fence_proxy_async_smem();  // the last answer has been read
@@ -615,19 +613,20 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                         }
                     }
                     sound = __all_sync(0xffffffffu, sound && !*abort_flag);
-                    if (!sound) break;
-                    if (!asked) claim();
-                    sound = __all_sync(0xffffffffu, wait(clc, claims & 1));
-                    if (!sound) break;
+                    if (sound) {
+                        if (!asked) claim();
+                        sound = __all_sync(0xffffffffu, wait(clc, claims & 1));
+                    }
+                    if (!sound) {  // an answer on its way lands before the CTA (and its shared memory) goes
+                        if (asked) mbar_wait(clc, claims & 1, wl);
+                        break;
+                    }
                     ++claims;
-                    asked = false;
                     more = canceled(sm + Sh::kOffClc, x, y, z);
                     __syncwarp();
                 }
             }
             if (!sound && lane == 0) give_up();
-            // an answer on its way lands before the CTA (and its shared memory) goes
-            if (asked) mbar_wait(clc, claims & 1, wl);
             __syncwarp();
         } else if (warp != kMmaWarp) {
             // ======================================================= load warps
