@@ -13,10 +13,11 @@
 //   * q_d = qs * (65536 a + 256 b + c), signed digits, qs = 2^-21 of the power of
 //     two of max|q|: elements down to 2^-11 (fp16) or 2^-14 (bf16) of it are exact;
 //   * w_t = p_t v_scale_t / (the tile's largest one) = (65536 a + 256 b + c) /
-//     8388607, unsigned digits: 23 bits of the tile's largest weight. The
-//     block scales are folded in here, and the tile's largest weight is the
-//     unit, so a tile's sum is exact to 2^-17 of itself whatever the others
-//     hold; tiles are joined in fp32.
+//     8388607, unsigned digits: 23 bits of the tile's largest weight, each off by
+//     2^-24 of it (as fp32 holds that largest one), which makes digits the bits
+//     of a sum's mantissa. The block scales are folded in here, and the tile's
+//     largest weight is the unit, so a tile's sum is exact to 2^-17 of itself
+//     whatever the others hold; tiles are joined in fp32.
 // Scores, running maxima and sums are fp32 (log2 domain).
 //
 // A work item is a (sequence, kv head, up to 8 of its query heads[,
@@ -849,19 +850,22 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
             for (int j = 0; j < ntiles; ++j, ++t) {
                 float *wm = wmax + (t & 1) * 4 * kV;
                 sound = __all_sync(0xffffffffu, sound && wait(s_full + (t & 1), (t >> 1) & 1));
-                float x[kSV];  // log2 of the weight
+                // log2 of the weight is score + lv. Their sum is rounded at the score's size,
+                // so it only finds a unit for the tile; the weights are formed from their
+                // distances to it, which are as small as the sums' from m_l (the sum's
+                // rounding alone cost a softmax of one token 4e-5 at scores of 1000).
+                float score[kSV], lv = 0.f;
                 if (sound) {
                     fence_after();
                     const Scales &sc = scales[t % kScales];
                     const float ks = sc.k[block], vs = sc.v[block];
                     const unsigned valid = sc.valid;
-                    const float lv = vs > 0.f ? log2f(vs) : -INFINITY;
+                    lv = vs > 0.f ? log2f(vs) : -INFINITY;
                     const int tok = first + j * kTok + r * kPar;
                     // (the same in every thread)
                     const bool whole = first + (j + 1) * kTok <= L && valid == (1u << blocks) - 1u;
                     int c[kCols3];
                     tmem_load<kCols3>(tlane + Sh::kSCol + (t & 1) * kN + 3 * v0, c);
-                    float score[kSV];
                     if constexpr (kSV % 2 == 0) {
 #pragma unroll
                         for (int v = 0; v < kSV; v += 2)
@@ -905,21 +909,31 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
 #pragma unroll
                         for (int v = 0; v < kSV; v += 2) {
                             (Pair(l[v], l[v + 1]) + Pair(fast_exp2(over[v]), fast_exp2(over[v + 1]))).get(l[v], l[v + 1]);
-                            (Pair(score[v], score[v + 1]) + Pair(lv)).get(x[v], x[v + 1]);
                         }
                     } else {
 #pragma unroll
-                        for (int v = 0; v < kSV; ++v) {
-                            l[v] += fast_exp2(over[v]);
-                            x[v] = score[v] + lv;
-                        }
+                        for (int v = 0; v < kSV; ++v) l[v] += fast_exp2(over[v]);
                     }
-                    // the tile's largest weight per head, over this warp
+                    // the tile's largest weight per head, over this warp, and a little above
+                    // it: more than the roundings of x, of the unit and of the distances to
+                    // it, so that no weight is above its unit.
+                    float x[kSV];
+                    const float lx = lv + 0x1p-16f;
+                    if constexpr (kSV % 2 == 0) {
+#pragma unroll
+                        for (int v = 0; v < kSV; v += 2) (Pair(score[v], score[v + 1]) + Pair(lx)).get(x[v], x[v + 1]);
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < kSV; ++v) x[v] = score[v] + lx;
+                    }
+                    float mw = 0.f;  // lane v has head v's
 #pragma unroll
                     for (int v = 0; v < kSV; ++v) {
-                        const float mw = warp_max(x[v]);
-                        if (lane == 0) wm[quarter * kV + v0 + v] = mw;
+                        const float m = warp_max(x[v]);
+                        mw = lane == v ? m : mw;
                     }
+                    // (without a weight it is -inf, which gives NaN here and so kNone)
+                    if (lane < kSV) wm[quarter * kV + v0 + lane] = fmaxf(fmaf(fabsf(mw), 0x1p-22f, mw), kNone);
                 }
                 ok = sync_and<kSoftmaxThreads>(sound);
                 if (!ok) break;
@@ -944,8 +958,6 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                 };
                 float mt[kSV];
                 tile_max(mt, v0);
-#pragma unroll
-                for (int v = 0; v < kSV; ++v) mt[v] = fmaxf(mt[v], kNone);  // finite, though the weights all be 0
                 if (j > 0) {  // O of the tile before is there: P and O are free once it is added up
                     sound = __all_sync(0xffffffffu, wait(o_full, (t - 1) & 1));
                     if (!sound) continue;  // (the next barrier tells the others)
@@ -957,8 +969,6 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                     for (int g = 0; g < kOG; ++g) m_tile[g] = mt[g];
                 } else {
                     tile_max(m_tile, vo);
-#pragma unroll
-                    for (int g = 0; g < kOG; ++g) m_tile[g] = fmaxf(m_tile[g], kNone);
                 }
                 // ---- the weights' digits, row 3 v + i, byte r of the row (its 16-byte chunks swizzled)
                 // (a whole number is the sum's mantissa: no conversion; bit 23 is 0 in its exponent)
@@ -966,12 +976,12 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                 if constexpr (kSV % 2 == 0) {
 #pragma unroll
                     for (int v = 0; v < kSV; v += 2) {
-                        fma2(Pair(mt[v], mt[v + 1]), Pair(-1.f), Pair(x[v], x[v + 1])).get(w[v], w[v + 1]);
+                        (fma2(Pair(mt[v], mt[v + 1]), Pair(-1.f), Pair(score[v], score[v + 1])) + Pair(lv)).get(w[v], w[v + 1]);
                         fma2(Pair(fast_exp2(w[v]), fast_exp2(w[v + 1])), Pair(kWUnit), Pair(8388608.f)).get(w[v], w[v + 1]);
                     }
                 } else {
 #pragma unroll
-                    for (int v = 0; v < kSV; ++v) w[v] = fmaf(fast_exp2(x[v] - mt[v]), kWUnit, 8388608.f);
+                    for (int v = 0; v < kSV; ++v) w[v] = fmaf(fast_exp2((score[v] - mt[v]) + lv), kWUnit, 8388608.f);
                 }
 #pragma unroll
                 for (int v = 0; v < kSV; ++v) {
