@@ -678,6 +678,11 @@ int pa_append_q8b(const void *key, const void *value, pa_dtype src_dtype, const 
  * query is q_dtype (PA_F16 or PA_BF16); out_dtype q_dtype or PA_F32.
  * max_context_len (at most 2^30) bounds every context_lens[s] (longer ones are
  * clamped, PA_DEVERR_CONTEXT); the closer the bound, the better the split.
+ * The query enters as fixed point: elements down to 2^-11 (PA_F16) or 2^-14
+ * (PA_BF16) of their head's largest are exact, and the smaller ones' errors
+ * add up to 2^-18 of the largest at most, or, where that would be more than
+ * about 2^-20 of the others' sum, to 2^-37 of it (a head whose largest is
+ * below 2^-100 counts as zero). The products' sums are exact, then fp32.
  * A query row that is not finite gives a NaN output row. workspace (nullable
  * device buffer, 16-byte aligned, of at least pa_decode_q8b_workspace_bytes,
  * else PA_ERR_WORKSPACE) lets a batch of few, long sequences be split along

@@ -11,7 +11,11 @@
 // as tcgen05.mma kind::i8 with exact int32 sums. Query and probabilities enter
 // as fixed point in base 256, three columns a head:
 //   * q_d = qs * (65536 a + 256 b + c), signed digits, qs = 2^-21 of the power of
-//     two of max|q|: elements down to 2^-11 (fp16) or 2^-14 (bf16) of it are exact;
+//     two of max|q|: elements down to 2^-11 (fp16) or 2^-14 (bf16) of it are exact.
+//     Where the others lose too much (a few elements 100 times as large as they
+//     are or more), what they lose is three more columns in a unit of its own.
+//     (Without them scores were off by 2e-4 where four elements of 128 were 1000
+//     times the others and met zeros in K: 2^-22 of max|q| for each of the others);
 //   * w_t = p_t v_scale_t / (the tile's largest one) = (65536 a + 256 b + c) /
 //     8388607, unsigned digits: 23 bits of the tile's largest weight, each off by
 //     2^-24 of it (as fp32 holds that largest one), which makes digits the bits
@@ -107,6 +111,8 @@ constexpr float kWUnit = 8388607.f;            // 2^23 - 1
 constexpr float kNone = -3e38f;                // below every score: the maximum of no tokens
 constexpr float kRaise = 16.f;                 // see the softmax
 
+constexpr int kWide = 1 << 8;                  // see the item warp
+
 // An item, as warp 7 hands it to the others.
 struct Item {
     int ntiles;   // -1: no more items
@@ -116,7 +122,7 @@ struct Item {
     int first;    // its tokens: first .. end - 1
     int end;
     int part;
-    int pad;
+    int heads;    // its query heads that there are, plus kWide if what their digits lose has columns, too
     int ids[kMaxBlocks];  // blocks of the first tile (-1: none)
 };
 
@@ -126,10 +132,12 @@ struct Scales {
     unsigned pad[3];
 };
 
-// V: virtual heads of an item (query heads, twice that at head_dim 64). The
-// digit rows a product reads past 3 V (up to kN) only give columns that nobody
+// V: virtual heads of an item (query heads, twice that at head_dim 64); kLone: one
+// query head, which has digit rows for what its digits lose, too. The digit rows a
+// product reads past the last one (up to kN) only give columns that nobody
 // reads, so those rows are whatever lies behind.
-template <int V> struct Shape {
+template <int V, bool kLone> struct Shape {
+    static constexpr int kQueries = kLone ? 2 * V : V;         // query columns, three digits each
     // softmax warpgroups: two halve the heads, and so a tile's time, where that bounds
     static constexpr int kTeams = V >= kTwoTeams ? 2 : 1;
     static constexpr int kSoftmaxThreads = 128 * kTeams, kThreads = kSoftmaxThreads + 128;
@@ -142,15 +150,16 @@ template <int V> struct Shape {
     // kStages is computed, and that was issued after O of the tile two before,
     // whose scales have been read
     static constexpr int kScales = kStages + 2;
-    static constexpr int kDigits = (3 * V + 7) / 8 * 1024;     // bytes of 3 V digit rows, in 8-row groups
+    static constexpr int kDigits = (3 * V + 7) / 8 * 1024;     // bytes of the weights' 3 V digit rows, in 8-row groups
+    static constexpr int kQDigits = (3 * kQueries + 7) / 8 * 1024;  // and the query's
     static constexpr int kOffK = 0;
     static constexpr int kOffV = kOffK + kStages * kTile;
     static constexpr int kOffQ = kOffV + kStages * kTile;      // [kItems] signed digits
-    static constexpr int kOffP = kOffQ + kItems * kDigits;     // unsigned digits; at an item's end at head_dim 64 the odd tokens' sums
+    static constexpr int kOffP = kOffQ + kItems * kQDigits;     // unsigned digits; at an item's end at head_dim 64 the odd tokens' sums
     static constexpr int kOffScales = kOffP + kDigits;
     static constexpr int kOffItems = kOffScales + kScales * (int)sizeof(Scales);
-    static constexpr int kOffQs = kOffItems + kItems * (int)sizeof(Item);  // float [kItems][V]: log2 score per digit unit
-    static constexpr int kOffMax = (kOffQs + kItems * V * 4 + 15) / 16 * 16;  // float [2][4 warps][V], tiles in turn
+    static constexpr int kOffQs = kOffItems + kItems * (int)sizeof(Item);  // float [kItems][kQueries]: log2 score per digit unit
+    static constexpr int kOffMax = (kOffQs + kItems * kQueries * 4 + 15) / 16 * 16;  // float [2][4 warps][V], tiles in turn
     static constexpr int kOffSums = (kOffMax + 8 * V * 4 + 15) / 16 * 16;  // float [2][4 warps][V]: the threads' sums
     static constexpr int kOffClc = (kOffSums + 8 * V * 4 + 15) / 16 * 16;
     static constexpr int kOffBar = kOffClc + 16;
@@ -163,11 +172,15 @@ template <int V> struct Shape {
     static constexpr int kCols = 3 * kN <= 64 ? 64 : 3 * kN <= 128 ? 128 : 256;
     // CTAs per SM: three, by shared memory; two with two softmax warpgroups
     static constexpr int kCtas = kTeams == 1 ? 3 : 2;
-    // registers: of the launch, and after the last four warps have given theirs to the softmax
-    static constexpr int kRegs = 80, kRegsLow = 40, kRegsHigh = kTeams == 1 ? 120 : 96;
+    // registers: of the launch, and after the last four warps have given theirs to the softmax: as many as spare
+    // both all spills (a spill is a trip to L2: with 40 and 120, 48 and 96, 12 and 28 words of them, 111
+    // sequences of up to 432 tokens, 32 heads x 6, 37.3 us, 34.8 without)
+    static constexpr int kRegs = 80, kRegsLow = 64, kRegsHigh = kTeams == 1 ? 96 : 88;
     static_assert(kRegsLow + kTeams * kRegsHigh <= (kTeams + 1) * kRegs, "registers taken over are registers given up");
     static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "CTAs per SM");
     static_assert(kCtas * kCols <= 512 && (kCtas + 1) * kRegs * kThreads > 65536, "tensor memory for every resident CTA");
+    static_assert(sizeof(Item) <= 32 * 4, "an item is copied by a warp");
+    static_assert(3 * kQueries <= kN, "a column for every digit");
     static_assert((V / 2) * 64 * 4 <= kDigits, "the odd tokens' sums fit the weights' digits");
 };
 
@@ -323,6 +336,14 @@ __device__ __forceinline__ void load_once(void *dst, const CUtensorMap *map, int
 template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
+// a[1], a[2], .., a[0]
+template <typename T, int N> __device__ __forceinline__ void turn(T (&a)[N]) {
+    const T first = a[0];
+#pragma unroll
+    for (int i = 0; i + 1 < N; ++i) a[i] = a[i + 1];
+    a[N - 1] = first;
+}
+
 // Asks for a block of the grid that has not started; the 16-byte answer completes on bar.
 __device__ __forceinline__ void try_cancel(void *answer, uint64_t *bar) {
     asm volatile(
@@ -356,12 +377,12 @@ __device__ __forceinline__ bool canceled(const void *answer, int &x, int &y, int
 // ------------------------------------------------------------------- kernel
 
 template <typename T, int D, int G, bool kHook = false>
-__global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128 / D)>::kCtas)
+__global__ void __launch_bounds__(Shape<G * (128 / D), G == 1>::kThreads, Shape<G * (128 / D), G == 1>::kCtas)
     decode_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                   const DecodeParams p) {
     constexpr int kPar = 128 / D;   // tokens per row
     constexpr int kV = G * kPar;    // virtual heads: par * G + g
-    using Sh = Shape<kV>;
+    using Sh = Shape<kV, G == 1>;
     constexpr int kN = Sh::kN, kStages = Sh::kStages, kScales = Sh::kScales, kTeams = Sh::kTeams;
     constexpr int kSoftmaxThreads = Sh::kSoftmaxThreads, kMmaWarp = Sh::kMmaWarp, kLoadV = Sh::kLoadV;
     constexpr int kSV = kV / kTeams, kOG = G / kTeams;  // virtual heads of a softmax thread, and heads whose O it adds up
@@ -369,6 +390,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
     constexpr int kOCols3 = (3 * kOG + 3) / 4 * 4; // O columns read: those of the lane's own tokens
     constexpr int kTok = 128 * kPar;              // tokens per tile
     constexpr int kItems = Sh::kItems;
+    constexpr int kHalf = G > 1 ? G / 2 : 1;       // heads of a part of an item in two (see the item warp)
 
     extern __shared__ __align__(1024) unsigned char sm[];
     unsigned char *Ps = sm + Sh::kOffP;
@@ -460,11 +482,9 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
             int tiles = 0;  // of all items so far
             // n: items handed on (a partition past its sequence's end is dropped here), claims: answers asked for
             for (int n = 0, claims = 0; sound;) {
-                const int slot = n % kItems;
-                Item &it = items[slot];
                 auto slot_free = [&]() {
                     if (n >= kItems)
-                        sound = __all_sync(0xffffffffu, wait(i_empty + slot, (n / kItems - 1) & 1));
+                        sound = __all_sync(0xffffffffu, wait(i_empty + n % kItems, (n / kItems - 1) & 1));
                     return sound;
                 };
                 bool asked = false;  // and not answered
@@ -480,9 +500,9 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                     allow_next();
                     if (!slot_free()) break;
                     if (lane == 0) {
-                        it.ntiles = -1;
-                        mbar_arrive(i_full + slot);
-                        mbar_arrive(q_full + slot);
+                        items[n % kItems].ntiles = -1;
+                        mbar_arrive(i_full + n % kItems);
+                        mbar_arrive(q_full + n % kItems);
                     }
                     break;
                 }
@@ -499,17 +519,14 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                 }
                 const int kvh = y / p.sub_groups, sub = y % p.sub_groups;
                 const int head0 = kvh * p.group + sub * kG, g_valid = min(G, p.group - sub * kG);
-                // the query's raw values, while the lengths come
+                // the query's raw values, while the lengths come (heads past the last one: that one's)
                 constexpr int kE = D / 32;
                 using Raw = std::conditional_t<kE == 4, uint2, uint32_t>;  // a lane's kE values
                 Raw raw[G];
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    raw[g] = Raw{};
-                    if (g < g_valid)
-                        raw[g] = reinterpret_cast<const Raw *>(static_cast<const T *>(p.query) +
-                                                               ((size_t)s * p.num_heads + head0 + g) * D)[lane];
-                }
+                for (int g = 0; g < G; ++g)
+                    raw[g] = reinterpret_cast<const Raw *>(static_cast<const T *>(p.query) +
+                                                           ((size_t)s * p.num_heads + head0 + min(g, g_valid - 1)) * D)[lane];
                 const int first = x * p.partition_size;
                 const int lb = (first >> bs_shift) + lane;
                 int id = lane < blocks && lb < p.max_blocks ? p.tables[(size_t)s * p.max_blocks + lb] : -1;
@@ -526,45 +543,54 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                 if (!real) L = first;
                 const int ntiles = L > first ? (L - first + kTok - 1) / kTok : 0;
                 if (lb >= (L + (1 << bs_shift) - 1) >> bs_shift) id = -1;
-                if (real) {
-                    if (!slot_free()) break;
-                    if (lane < kMaxBlocks) it.ids[lane] = id;
+                if (real && slot_free()) {
+                    int slot = n % kItems;
+                    Item *it = items + slot;
+                    if (lane < kMaxBlocks) it->ids[lane] = id;
                     if (lane == 0) {
-                        it.ntiles = ntiles;
-                        it.s = s;
-                        it.head0 = head0;
-                        it.kvh = kvh;
-                        it.first = first;
-                        it.end = L;
-                        it.part = x;
+                        it->ntiles = ntiles;
+                        it->s = s;
+                        it->head0 = head0;
+                        it->kvh = kvh;
+                        it->first = first;
+                        it->end = L;
+                        it->part = x;
+                        it->heads = g_valid;
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(i_full + slot);  // the load warps can start
                     tiles += ntiles;
                     if (p.steal && __all_sync(0xffffffffu, tiles - *loaded <= kClaimAhead)) claim();
                     // ---- the query's digits
-                    unsigned char *Qs = sm + Sh::kOffQ + slot * Sh::kDigits;
-                    uint32_t mag[G];  // the largest |q|, as its bits (they order like the values, infinities and NaN on top)
-#pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        const uint32_t *w = reinterpret_cast<const uint32_t *>(&raw[g]);
-                        uint32_t m = w[0] & 0x7fff7fffu;
-                        if constexpr (kE == 4) m = __vmaxu2(m, w[1] & 0x7fff7fffu);
-                        mag[g] = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xffffu));
-                    }
-#pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        const T *raw_g = reinterpret_cast<const T *>(&raw[g]);
-                        const unsigned short bits = (unsigned short)mag[g];
-                        const uint32_t e = __float_as_uint((float)*reinterpret_cast<const T *>(&bits)) >> 23;  // its exponent
-                        const bool finite = e < 255u;
-                        // a query below 2^-100 counts as zero (its unit's reciprocal would not be finite)
-                        const bool live = finite && e >= 27u;
-                        const float inv = live ? __uint_as_float((275u - e) << 23) : 0.f;
+                    constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: a sum with it is a whole number below 2^22, in its bits
+                    // the largest of two magnitudes in a word (16-bit ones order like the values, infinities and NaN on top)
+                    auto larger = [](uint32_t m) { return max(m >> 16, m & 0xffffu); };
+                    // a lane's largest |q| of a head
+                    auto lanes = [&](const Raw &raw) -> uint32_t {
+                        const uint32_t *w = reinterpret_cast<const uint32_t *>(&raw);
+                        if constexpr (kE == 4) return larger(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu));
+                        else return larger(w[0] & 0x7fff7fffu);
+                    };
+                    auto as_float = [](uint32_t m) -> uint32_t {  // its fp32 bits
+                        const unsigned short bits = (unsigned short)m;
+                        return __float_as_uint((float)*reinterpret_cast<const T *>(&bits));
+                    };
+                    auto largest = [&](const Raw &raw) { return as_float(__reduce_max_sync(0xffffffffu, lanes(raw))); };
+                    // The digits' unit for that largest magnitude, and its reciprocal; 0 and 0 below 2^-100, which
+                    // counts as zero (the reciprocal would not be finite). Returns whether it is finite.
+                    auto units = [](uint32_t bits, float &unit, float &inv) {
+                        const uint32_t e = bits >> 23;
+                        const bool live = e < 255u && e >= 27u;
+                        unit = live ? __uint_as_float((e - 21u) << 23) : 0.f;
+                        inv = live ? __uint_as_float((275u - e) << 23) : 0.f;
+                        return e < 255u;
+                    };
+                    // the digits of whole numbers (with kWhole added) as query column col, in units of `unit`
+                    auto put = [&](int col, const float (&t)[kE], float unit) {
+                        unsigned char *Qs = sm + Sh::kOffQ + slot * Sh::kQDigits;
                         uint32_t u[kE];  // the digits, plus 128 each
 #pragma unroll
-                        for (int i = 0; i < kE; ++i)
-                            u[i] = __float_as_uint(fmaf((float)raw_g[i], inv, 12582912.f)) + 0x408080u;
+                        for (int i = 0; i < kE; ++i) u[i] = __float_as_uint(t[i]) + 0x408080u;
                         uint32_t w[3];  // the lane's kE digits of each place
                         if constexpr (kE == 4) {
                             const uint32_t lo01 = __byte_perm(u[0], u[1], 0x5140), lo23 = __byte_perm(u[2], u[3], 0x5140);
@@ -578,11 +604,12 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                         }
 #pragma unroll
                         for (int i = 0; i < 3; ++i) w[i] ^= 0x80808080u;
+                        auto place = [&](int par) { return G == 1 ? col * kPar + par : par * G + col; };
 #pragma unroll
                         for (int par = 0; par < kPar; ++par)
 #pragma unroll
                             for (int i = 0; i < 3; ++i) {
-                                const int r = (par * G + g) * 3 + i;  // digit row; its 16-byte chunks are swizzled
+                                const int r = place(par) * 3 + i;  // digit row; its 16-byte chunks are swizzled
                                 auto at = [&](int half) {
                                     return Qs + r * kRowBytes + ((half * D + lane * kE) ^ ((r & 7) << 4));
                                 };
@@ -593,20 +620,122 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                                     *reinterpret_cast<uint16_t *>(at(1 - par)) = 0;
                                 }
                             }
-                        // (a query that is not finite makes its scores, and so its row, NaN)
-                        if (lane < kPar)
-                            qscale[slot * kV + lane * G + g] = live ? __uint_as_float((e - 21u) << 23) * p.scale_log2
-                                                                    : finite ? 0.f : NAN;
+                        if (lane < kPar) qscale[slot * Sh::kQueries + place(lane)] = unit * p.scale_log2;
+                    };
+                    uint32_t mag[G];
+                    bool wide = false;
+                    // How many lanes have an element below the exact ones, and one of 2^-7 of the largest or
+                    // more: a byte a head, four heads a sum over the warp.
+                    uint32_t below = 0, above = 0;
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        constexpr int kExponent = std::is_same_v<T, __half> ? 10 : 7, kExact = std::is_same_v<T, __half> ? 11 : 14;
+                        constexpr uint32_t kFew = std::is_same_v<T, __half> && kE == 4 ? 4 : 2;  // such lanes that do no harm
+                        const uint32_t *w = reinterpret_cast<const uint32_t *>(&raw[g]);
+                        uint32_t least = w[0] & 0x7fff7fffu;
+                        if constexpr (kE == 4) least = __vminu2(least, w[1] & 0x7fff7fffu);
+                        const int most = lanes(raw[g]), top = __reduce_max_sync(0xffffffffu, most);
+                        below += (int)min(least >> 16, least & 0xffffu) < top - (kExact << kExponent) ? 1u << 8 * (g % 4) : 0u;
+                        above += most >= top - (7 << kExponent) ? 1u << 8 * (g % 4) : 0u;
+                        mag[g] = as_float(top);
+                        if (g % 4 == 3 || g == G - 1) {
+                            below = __reduce_add_sync(0xffffffffu, below);
+                            above = __reduce_add_sync(0xffffffffu, above);
+                            // (a byte's top bit) more than a few are below, or one is and fewer than 16 are above
+                            wide |= (((below + (0x7f - kFew) * 0x01010101u) | ((below + 0x7f7f7f7fu) & ~(above + 0x70707070u))) & 0x80808080u) != 0;
+                            below = above = 0;
+                        }
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(q_full + slot);
-                    ++n;
+                    // Then whether a head's digits lose more than 2^-21 of the sum of its elements below 2^17 units (a
+                    // sixteenth of the largest), by one sum over the warp, of 256ths of a unit lost and 256s of units
+                    // there. (Queries whose elements are less than some 50 times apart hardly ever come here, so that
+                    // these instructions are not at hand. A few lanes' elements lose 2^-18 of the largest at most.)
+                    if (__builtin_expect(wide, 0)) {
+                        wide = false;
+#pragma unroll 1
+                        for (int g = 0; g < G; ++g) {  // (head 0 of the arrays, which turn: the loop's code stays small)
+                            float unit, inv, gone = 0.f, there = 0.f;
+                            units(mag[0], unit, inv);
+#pragma unroll
+                            for (int i = 0; i < kE; ++i) {
+                                const float q = (float)reinterpret_cast<const T *>(&raw[0])[i], t = fmaf(q, inv, kWhole);
+                                gone += fabsf(fmaf(q, inv, kWhole - t));
+                                there += fabsf(t - kWhole) < 131072.f ? fabsf(t - kWhole) : 0.f;
+                            }
+                            const uint32_t sums = __reduce_add_sync(0xffffffffu, (uint32_t)(gone * 256.f) << 17 | (uint32_t)there >> 8);
+                            wide |= (sums >> 17) * 32u > (sums & 0x1ffffu);
+                            turn(raw);
+                            turn(mag);
+                        }
+                        wide = wide && ntiles > 0;
+                    }
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        float unit, inv, t[kE];
+                        const bool finite = units(mag[g], unit, inv);
+#pragma unroll
+                        for (int i = 0; i < kE; ++i) t[i] = fmaf((float)reinterpret_cast<const T *>(&raw[g])[i], inv, kWhole);
+                        put(g, t, finite ? unit : NAN);  // (a query that is not finite makes its scores, and so its row, NaN)
+                    }
+                    // Then what they lose has digits of its own: beside the others where there is one head, else in
+                    // place of half of the heads, which become an item of their own.
+                    for (int left = wide ? it->heads : 0; __builtin_expect(left > 0, 0);) {
+                        const int now = min(left, kHalf);
+                        Raw part[kHalf];
+#pragma unroll
+                        for (int g = 0; g < kHalf; ++g)
+                            part[g] = reinterpret_cast<const Raw *>(static_cast<const T *>(p.query) +
+                                                                    ((size_t)it->s * p.num_heads + it->head0 + min(g, now - 1)) * D)[lane];
+#pragma unroll 1
+                        for (int g = 0; g < kHalf; ++g) {
+                            float unit, inv, t[kE], rest[kE];
+                            const bool finite = units(largest(part[0]), unit, inv);
+                            uint32_t m = 0;
+#pragma unroll
+                            for (int i = 0; i < kE; ++i) {
+                                const float q = inv > 0.f ? (float)reinterpret_cast<const T *>(&part[0])[i] : 0.f;
+                                t[i] = fmaf(q, inv, kWhole);
+                                rest[i] = fmaf(kWhole - t[i], unit, q);  // exact
+                                m = max(m, __float_as_uint(fabsf(rest[i])));
+                            }
+                            put(g, t, finite ? unit : NAN);
+                            units(__reduce_max_sync(0xffffffffu, m), unit, inv);
+#pragma unroll
+                            for (int i = 0; i < kE; ++i) t[i] = fmaf(rest[i], inv, kWhole);
+                            put(g + kHalf, t, unit);
+                            turn(part);
+                        }
+                        if (lane == 0) it->heads = now + kWide;
+                        left -= now;
+                        if (left <= 0) break;
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(q_full + slot);
+                        ++n;
+                        if (!slot_free()) break;
+                        const Item *before = it;
+                        slot = n % kItems;
+                        it = items + slot;
+                        // (its fields are as before, but the head)
+                        if (lane < (int)(sizeof(Item) / 4))
+                            reinterpret_cast<int *>(it)[lane] = reinterpret_cast<const int *>(before)[lane];
+                        __syncwarp();
+                        if (lane == 0) it->head0 += kHalf;
+                        tiles += it->ntiles;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(i_full + slot);
+                    }
+                    if (sound) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(q_full + slot);
+                        ++n;
+                    }
                 }
                 // ---- the next one, once few tiles are left to load
                 more = false;
                 if (p.steal) {
-                    if (!asked && tiles - *loaded > kClaimAhead) {
+                    if (sound && !asked && tiles - *loaded > kClaimAhead) {
                         const uint64_t t0 = global_ns();
                         for (uint32_t i = 1; sound && tiles - *loaded > kClaimAhead; ++i) {
                             __nanosleep(64);
@@ -753,7 +882,7 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
                         if (!sound) break;
                         fence_after();
                         const uint32_t ka = desc128(base + Sh::kOffK) + b * (kTile / 16);
-                        const uint32_t qa = desc128(base + Sh::kOffQ) + slot * (Sh::kDigits / 16);
+                        const uint32_t qa = desc128(base + Sh::kOffQ) + slot * (Sh::kQDigits / 16);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             mma_i8(tmem + Sh::kSCol + (issued & 1) * kN, ka + kk * 2, qa + kk * 2, kIdQK,
@@ -810,10 +939,10 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
             }
             const int L = it.end, first = it.first, part = it.part;
             const size_t row0 = (size_t)it.s * p.num_heads + it.head0;  // output row of head 0
-            const int g_valid = min(G, p.group - it.head0 % p.group / kG * kG);
+            const int g_valid = it.heads & (kWide - 1);
             float qs[kSV];
 #pragma unroll
-            for (int v = 0; v < kSV; ++v) qs[v] = qscale[slot * kV + v0 + v];
+            for (int v = 0; v < kSV; ++v) qs[v] = qscale[slot * Sh::kQueries + v0 + v];
             float m_l[kSV], l[kSV];                // this thread's tokens: about their largest score, sum of 2^(score - it)
             float m_o[kOG], o[kOG], m_tile[kOG];   // O of the lane's dim: sum * 2^-m_o; the unit of the tile in tensor memory
 #pragma unroll
@@ -874,6 +1003,20 @@ __global__ void __launch_bounds__(Shape<G * (128 / D)>::kThreads, Shape<G * (128
 #pragma unroll
                         for (int v = 0; v < kSV; ++v)
                             score[v] = number(c[3 * v], c[3 * v + 1], c[3 * v + 2]) * (qs[v] * ks);
+                    }
+                    if (__builtin_expect(it.heads >= kWide, 0)) {  // what the digits lose (looked up: no register lives for it)
+                        if constexpr (G == 1) {
+                            tmem_load<kCols3>(tlane + Sh::kSCol + (t & 1) * kN + 3 * kV, c);
+#pragma unroll
+                            for (int v = 0; v < kSV; ++v)
+                                score[v] += number(c[3 * v], c[3 * v + 1], c[3 * v + 2]) * (qscale[slot * Sh::kQueries + kV + v] * ks);
+                        } else {  // (kSV is a multiple of G)
+#pragma unroll
+                            for (int v = 0; v < kSV; ++v) {
+                                if (v % G < kHalf) score[v] += score[v + kHalf];
+                                else score[v] = -INFINITY;
+                            }
+                        }
                     }
                     if (!whole) {
 #pragma unroll
@@ -1149,7 +1292,7 @@ template <int D, int kJoinWarps> __global__ void __launch_bounds__(kJoinWarps * 
 
 template <typename T, int D, int G, bool kHook = false>
 static cudaError_t launch_decode_t(const CUtensorMap &km, const CUtensorMap &vm, DecodeParams p, cudaStream_t stream) {
-    using Sh = Shape<G * (128 / D)>;
+    using Sh = Shape<G * (128 / D), G == 1>;
     auto kern = decode_kernel<T, D, G, kHook>;
     static AttrCache attr;
     static std::atomic<int> regs{0};

@@ -1,6 +1,6 @@
 """pa_decode_q8b and pa_append_q8b where they are easily wrong: a wait that runs
 out while further work has been claimed, softmaxes of one token, blocks that are
-all bad."""
+all bad, queries with a few large elements."""
 import math
 
 import numpy as np
@@ -109,3 +109,76 @@ def test_a_sequence_of_bad_blocks_alone_gives_zeros(pa, D, Hq, Hkv):
     d.tables[0, 8:-8] = d.tables[0, 16:].copy()
     d.ctx[:] = [172, 0, 5]
     d.check(out, torch.float16)
+
+
+def raised(D, Hq, Hkv, bs, lens, times, seed, qdt, heads=slice(None), spread=0.5, codes=0):
+    """A case whose queries have four elements `times` the size of the others, over codes of at most `codes` in K."""
+    rng = np.random.default_rng(seed)
+    c = Case(Hq, Hkv, D, bs, lens, seed=seed, spread=spread)
+    dims = rng.choice(D, 4, replace=False)
+    for d in dims:
+        c.q[:, heads, d] = c.q[:, heads, d].sign() * (0.5 + c.q[:, heads, d].abs() / 4) * times
+    c.kq[..., dims] = rng.integers(-codes, codes + 1, c.kq[..., dims].shape)
+    c.q = c.q.to(qdt).float()
+    return c
+
+
+@pytest.mark.parametrize("qdt,times", [(torch.float16, 1), (torch.float16, 30), (torch.float16, 100), (torch.float16, 1e3),
+                                       (torch.float16, 3e4), (torch.bfloat16, 1e3), (torch.bfloat16, 1e6)])
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 4, 4), (64, 4, 4), (128, 6, 3), (128, 6, 2), (64, 8, 2), (128, 16, 2), (64, 7, 1),
+                                      (128, 11, 1)])
+def test_scores_of_queries_with_few_large_elements(pa, qdt, times, D, Hq, Hkv):
+    """Two tokens with V opposite: out = M tanh((s0 - s1) / 2), so its error shows the scores'. A score is within 2^-20
+    of A = scale sum_d |q_d k_d|: a difference of two within 2^-19 A, half of which is the tanh's, at most; the powers of
+    two, weights and fp32 steps as for one token (2^-19)."""
+    S = 40
+    c = raised(D, Hq, Hkv, 16, [2] * S, times, seed=53, qdt=qdt, spread=0.2)
+    b = c.tables[:, 0]
+    c.vq[b, :, 0], c.vq[b, :, 1] = 127, -127
+    got = c.run(pa, qdt).double().cpu().numpy()
+    G = Hq // Hkv
+    k = c.kq[b][:, :, :2].astype(np.float64) * c.ks[b].astype(np.float64)[:, :, None, None]  # [S, Hkv, 2, D]
+    k = np.repeat(k, G, 1)
+    q = c.q.double().numpy()[:, :, None]
+    s = (q * k).sum(-1) * c.scale
+    A = (np.abs(q) * np.abs(k)).sum(-1).max(-1) * c.scale
+    M = np.repeat(127 * c.vs[b].astype(np.float64), G, 1)
+    err = np.abs(got - (M * np.tanh((s[..., 0] - s[..., 1]) / 2))[..., None]).max(-1)
+    assert (err <= M * (2.0 ** -20 * A + 2.0 ** -19)).all(), float((err / (M * (2.0 ** -20 * A + 2.0 ** -19))).max())
+    assert pa.pa_read_device_errors() == 0
+
+
+@pytest.mark.parametrize("qdt,times", [(torch.float16, 1e3), (torch.bfloat16, 1e5)])
+@pytest.mark.parametrize("D,bs,Hq,Hkv", [(128, 16, 2, 2), (64, 32, 2, 2), (128, 32, 10, 2), (64, 16, 8, 1), (128, 16, 6, 2),
+                                         (128, 16, 17, 1), (64, 32, 12, 4)])
+def test_decode_of_queries_with_few_large_elements(pa, qdt, times, D, bs, Hq, Hkv):
+    """All heads such, or one of a group; short and long, split and not, and more of them than CTAs."""
+    for heads in (slice(None), slice(Hq - 1, None), slice(0, None, 2)):
+        c = raised(D, Hq, Hkv, bs, [1, 17, 129, 300, 0, 2500], times, 55, qdt, heads=heads)
+        for kw in (dict(), dict(workspace=False), dict(max_ctx=9000)):
+            c.check(c.run(pa, qdt, **kw), qdt, f"{heads} {kw}")
+    lens = np.random.default_rng(56).integers(0, 300, 500)
+    c = raised(D, Hq, Hkv, bs, lens, times, 57, qdt)
+    c.q[::3] = torch.from_numpy(np.random.default_rng(58).normal(size=c.q[::3].shape)).to(qdt).float()
+    a = c.run(pa, qdt)
+    c.check(a, qdt, "many")
+    assert torch.equal(a, c.run(pa, qdt, workspace=False, order=np.random.default_rng(59).permutation(500)))
+    assert pa.pa_read_device_errors() == 0
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 2, 2), (64, 2, 2), (128, 4, 1), (64, 8, 1), (128, 8, 1)])
+def test_non_finite_queries_beside_ones_with_few_large_elements(pa, D, Hq, Hkv):
+    c = raised(D, Hq, Hkv, 16, [300, 40, 1], 1e3, 60, torch.float16)
+    want = c.run(pa, torch.float16)
+    c.check(want, torch.float16)
+    c.q[0, 1, 3], c.q[2, 0, 0] = math.nan, math.inf
+    got = c.run(pa, torch.float16)
+    bad = torch.zeros(got.shape[:2], dtype=torch.bool, device="cuda")
+    bad[0, 1] = bad[2, 0] = True
+    assert torch.isnan(got[bad]).all() and torch.isfinite(got[~bad]).all()
+    d = Case.__new__(Case)
+    d.__dict__.update(c.__dict__)
+    d.q = torch.where(bad.cpu()[..., None], torch.zeros(()), c.q)
+    ref, tol = d.ref(torch.float16)
+    assert (np.abs(got.double().cpu().numpy() - ref) <= tol)[~bad.cpu().numpy()].all()
+    assert pa.pa_read_device_errors() == 0
