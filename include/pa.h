@@ -665,7 +665,8 @@ int pa_dpool_release(void *state, int num_blocks, int block_size, int32_t *block
  * given each sequence its own last block). q_start must be non-decreasing
  * from 0 and at most num_tokens at its end. A sequence with q_len_s >
  * context_lens[s] or a context past its table row is skipped
- * (PA_DEVERR_CONTEXT), a block with a bad id as well (PA_DEVERR_BLOCK_ID).
+ * (PA_DEVERR_CONTEXT), a block with a bad id as well (PA_DEVERR_BLOCK_ID);
+ * one without new tokens is not looked at.
  */
 int pa_append_q8b(const void *key, const void *value, pa_dtype src_dtype, const int32_t *q_start, int num_tokens,
                   int8_t *k_cache, int8_t *v_cache, float *k_scale, float *v_scale, const int32_t *block_tables,

@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(kWarps * 32, AppendShape<T, D, BS, kByToken>::
     const int s = unit_seq<BS, kByToken>(p.q_start, p.num_seqs, u, lane);
     const int q0 = p.q_start[s], q1 = p.q_start[s + 1];
     const int ctx = p.ctx[s];
+    if (q0 == q1) return;  // nothing to write (such a sequence has units only where they are counted by blocks)
     const bool first_warp = blockIdx.y == 0 && threadIdx.x < 32;
     if (q0 < 0 || q1 < q0 || q1 > p.num_tokens || q1 - q0 > ctx || ctx > (long long)p.max_blocks * BS) {
         if (first_warp && lane == 0) record_error(p.err, PA_DEVERR_CONTEXT);

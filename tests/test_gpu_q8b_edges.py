@@ -1,13 +1,14 @@
 """pa_decode_q8b and pa_append_q8b where they are easily wrong: a wait that runs
 out while further work has been claimed, softmaxes of one token, blocks that are
-all bad, queries with a few large elements."""
+all bad, queries with a few large elements, lengths that
+are wrong where nothing is written."""
 import math
 
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_q8b import Case
+from test_gpu_q8b import Case, WriteCase
 
 pytestmark = pytest.mark.gpu
 
@@ -182,3 +183,19 @@ def test_non_finite_queries_beside_ones_with_few_large_elements(pa, D, Hq, Hkv):
     ref, tol = d.ref(torch.float16)
     assert (np.abs(got.double().cpu().numpy() - ref) <= tol)[~bad.cpu().numpy()].all()
     assert pa.pa_read_device_errors() == 0
+
+
+@pytest.mark.parametrize("pad", [0, 1, 40, 400])
+def test_write_does_not_look_at_sequences_without_new_tokens(pa, pad):
+    """Whether the work is dealt out by tokens or by blocks (as the padding has it): a length past the table row, or
+    below 0, is no error of a sequence that gets nothing, and is one of a sequence that does."""
+    old, new = [40, 3, 7, 30, 5, 9], [0, 2, 0, 1, 0, 0]
+    c = WriteCase(2, 64, 16, torch.float16, old, new, seed=61, pad=pad)
+    right = c.ctx.copy()
+    c.ctx[[0, 2, 5]] = [100000, -3, 2 ** 31 - 1]
+    d = c.run(pa)
+    assert pa.pa_read_device_errors() == 0
+    c.check(pa, d, ctx=right)
+    c.ctx[3] = 100000
+    c.run(pa)
+    assert pa.pa_read_device_errors() == 0x4
