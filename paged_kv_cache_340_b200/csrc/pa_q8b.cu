@@ -319,7 +319,9 @@ extern "C" int pa_append_q8b(const void *key, const void *value, pa_dtype src_dt
     if (src_dtype != PA_F32 && src_dtype != PA_F16 && src_dtype != PA_BF16) return PA_ERR_DTYPE;
     if (head_dim != 64 && head_dim != 128) return PA_ERR_HEAD_DIM;
     if (block_size != 16 && block_size != 32) return PA_ERR_BLOCK_SIZE;
-    if ((long long)num_blocks * block_size > INT32_MAX || num_tokens > INT32_MAX - 4 * 65536) return PA_ERR_SHAPE;
+    if ((long long)num_blocks * block_size > INT32_MAX || max_blocks_per_seq > INT32_MAX / block_size ||
+        num_tokens > INT32_MAX - 4 * 65536)
+        return PA_ERR_SHAPE;
     if (num_tokens == 0 || num_seqs == 0) return PA_OK;
     if (!key || !value || !q_start || !k_cache || !v_cache || !k_scale || !v_scale || !block_tables || !context_lens)
         return PA_ERR_NULL;

@@ -101,3 +101,10 @@ def test_copy_blocks_q8b_host_checks(pa, kw, code):
 @pytest.mark.parametrize("T", [(1 << 30) + 1, (1 << 31) - 1])
 def test_dpool_append_refuses_more_slots_than_it_can_number(pa, T):
     assert pa._lib.pa_dpool_append(A, 64, 16, A, 8, A, A, 4, A, A, T, A, A, None) == -3
+
+
+def test_append_q8b_refuses_tables_wider_than_its_positions(pa):
+    """Positions are 32-bit: a row of 2^27 blocks of 16 would reach 2^31."""
+    for mb, bs, code in ((1 << 27, 16, -3), (1 << 26, 32, -3), ((1 << 27) - 1, 16, 0), ((1 << 26) - 1, 32, 0)):
+        # (without tokens nothing is launched; the sizes are checked first)
+        assert pa._lib.pa_append_q8b(A, A, 1, A, 0, A, A, A, A, A, mb, A, 3, 40, 2, 128, bs, None) == code
