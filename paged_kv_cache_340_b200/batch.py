@@ -495,6 +495,9 @@ class ServingStep:
                  device="cuda", pool: Optional[DevicePool] = None, num_layers: int = 1):
         if num_layers < 1:
             raise ValueError("ServingStep: at least one layer")
+        if pool is not None and (pool.num_blocks, pool.block_size) != (num_blocks, block_size):
+            raise ValueError(f"ServingStep: the pool has {pool.num_blocks} blocks of {pool.block_size} tokens, the caches "
+                             f"{num_blocks} of {block_size}")
         i32 = dict(dtype=torch.int32, device=device)
         self.pool = pool if pool is not None else DevicePool(num_blocks, block_size, policy, device=device)
         self.block_tables = torch.full((num_seqs, max_blocks_per_seq), -1, **i32)

@@ -108,3 +108,13 @@ def test_append_q8b_refuses_tables_wider_than_its_positions(pa):
     for mb, bs, code in ((1 << 27, 16, -3), (1 << 26, 32, -3), ((1 << 27) - 1, 16, 0), ((1 << 26) - 1, 32, 0)):
         # (without tokens nothing is launched; the sizes are checked first)
         assert pa._lib.pa_append_q8b(A, A, 1, A, 0, A, A, A, A, A, mb, A, 3, 40, 2, 128, bs, None) == code
+
+
+@pytest.mark.parametrize("blocks,size", [(40, 32), (41, 16), (39, 16)])
+def test_serving_step_refuses_a_pool_of_other_sizes(pa, blocks, size):
+    """A pool of more blocks hands out ids that the caches do not have, one of other block size other slots."""
+    from types import SimpleNamespace
+
+    from paged_kv_cache_340_b200.batch import ServingStep
+    with pytest.raises(ValueError, match="pool"):
+        ServingStep(2, 4, 40, 16, 4, 2, 64, 10, device="cpu", pool=SimpleNamespace(num_blocks=blocks, block_size=size))
