@@ -35,6 +35,7 @@
 #include "pa_common.cuh"
 #include "pa_dpool.cuh"
 #include "pa_internal.h"
+#include "pa_pdl.cuh"
 
 namespace pa {
 namespace beam {
@@ -274,13 +275,6 @@ __device__ __forceinline__ void chunk_of(const StepParams &q, int *e0, int *e1) 
 }
 
 __device__ __forceinline__ volatile int *status_word(const Pool &p) { return p.tail; }
-
-// Programmatic dependent launch: launches 2-4 start while the previous one
-// runs (each stages the per-beam values, which no launch writes) and wait
-// for it to finish, its writes visible, before they read its results. Both
-// are no-ops for a launch made without the attribute.
-__device__ __forceinline__ void allow_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_previous_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---- phase 1 (count)
 __device__ void phase_count(const StepParams &q, const Pool &p, const Staged &st) {
@@ -570,13 +564,14 @@ __device__ void phase_finish(const StepParams &q, const Pool &p, const Staged &s
 }
 
 
-// ---- the four phases as four launches (launches 2-4 by programmatic
-// dependent launch)
+// ---- the four phases as four launches. Launches 2-4 (programmatic dependent
+// launch) start while the previous one runs, stage the per-beam values, which
+// no launch writes, and wait for it before they read its results.
 
 __global__ void __launch_bounds__(kStepThreads) beam_count_kernel(const StepParams q) {
     extern __shared__ int dyn[];
     __shared__ int s_bad;
-    allow_next_launch();
+    allow_next();
     const Pool p = views(q.state, q.num_blocks);
     const Staged st = stage_beams(q, p, dyn, &s_bad);
     phase_count(q, p, st);
@@ -587,10 +582,10 @@ __global__ void __launch_bounds__(kStepThreads) beam_count_kernel(const StepPara
         extern __shared__ int dyn[];                                                     \
         __shared__ int s_bad;                                                            \
         __shared__ int warp_sums[kStepThreads / 32];                                     \
-        if (ALLOW_NEXT) allow_next_launch();                                             \
+        if (ALLOW_NEXT) allow_next();                                                    \
         const Pool p = views(q.state, q.num_blocks);                                     \
         const Staged st = stage_beams(q, p, dyn, &s_bad);                                \
-        wait_previous_launch(); /* from here on: the previous launch's results */        \
+        wait_previous(); /* from here on: the previous launch's results */               \
         PHASE(q, p, st, warp_sums);                                                      \
     }
 PA_BEAM_PHASE_KERNEL(beam_flags_kernel, phase_flags, true)
@@ -1010,19 +1005,12 @@ cudaError_t launch_beam_step(int32_t *state, const int32_t *old_tables, const in
     beam::beam_count_kernel<<<grid, block, smem, stream>>>(q);  // after all earlier work on the stream
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, beam::beam_flags_kernel, q);
-    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, beam::beam_apply_kernel, q);
-    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, beam::beam_finish_kernel, q);
+    const auto next = [&](void (*kern)(const beam::StepParams)) {
+        return launch_after(kern, grid, block.x, (size_t)smem, 1, stream, q);
+    };
+    e = next(beam::beam_flags_kernel);
+    if (e == cudaSuccess) e = next(beam::beam_apply_kernel);
+    if (e == cudaSuccess) e = next(beam::beam_finish_kernel);
     return e;
 }
 
