@@ -486,7 +486,13 @@ class ServingStep:
     one stream; steps of one object must not overlap.
 
     A prompt's row is decoded for its last token like any other; rows of
-    length 0 give zeros. Check pa_read_device_errors() now and then: a step
+    length 0 give zeros. With more than one layer that is not all of a prompt's
+    attention: the next layer's key and value rows come from every prompt
+    token's, which the caller computes (one token a row needs no more than
+    attend gives). Sequences are forked outside, in tables, lengths and pool.
+    The host knows no lengths, so attend bounds them by the table's width, by
+    which long sequences are split, and gives no order: the narrower the table,
+    the better. Check pa_read_device_errors() now and then: a step
     that the pool has no room for appends nothing (q_start is all 0)."""
 
     def __init__(self, num_seqs: int, max_blocks_per_seq: int, num_blocks: int, block_size: int, num_heads: int,

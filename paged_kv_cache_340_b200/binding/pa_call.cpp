@@ -1,7 +1,7 @@
 // The serving step's calls from Python without ctypes: a step of small batches
 // takes its GPU 3 to 8 us a call, and one check per tensor and one conversion per
 // argument in Python took longer than that (pa_append_q8b for 64 single tokens:
-// 9.4 us a call, 3.2 of them on the GPU).
+// 9.2 us a call, 2.4 of them on the GPU).
 //
 // Each function takes its tensors as they are, checks their types, shapes,
 // layouts and device (ValueError), calls the C entry point of its name and
