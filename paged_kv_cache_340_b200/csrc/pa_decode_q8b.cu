@@ -172,9 +172,9 @@ template <int V, bool kLone> struct Shape {
     static constexpr int kCols = 3 * kN <= 64 ? 64 : 3 * kN <= 128 ? 128 : 256;
     // CTAs per SM: three, by shared memory; two with two softmax warpgroups
     static constexpr int kCtas = kTeams == 1 ? 3 : 2;
-    // registers: of the launch, and after the last four warps have given theirs to the softmax: as many as spare
-    // both all spills (a spill is a trip to L2: with 40 and 120, 48 and 96, 12 and 28 words of them, 111
-    // sequences of up to 432 tokens, 32 heads x 6, 37.3 us, 34.8 without)
+    // registers: of the launch, and after the last four warps have given theirs to the softmax. Split so that no warp
+    // spills, which is a trip to L2 (111 sequences of up to 432 tokens, 32 heads x 6: 34.8 us; with 40 left to the last
+    // four warps, 100 to 200 bytes of them spilled, 37.3)
     static constexpr int kRegs = 80, kRegsLow = 64, kRegsHigh = kTeams == 1 ? 96 : 88;
     static_assert(kRegsLow + kTeams * kRegsHigh <= (kTeams + 1) * kRegs, "registers taken over are registers given up");
     static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "CTAs per SM");

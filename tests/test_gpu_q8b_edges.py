@@ -199,3 +199,16 @@ def test_write_does_not_look_at_sequences_without_new_tokens(pa, pad):
     c.ctx[3] = 100000
     c.run(pa)
     assert pa.pa_read_device_errors() == 0x4
+
+
+@pytest.mark.parametrize("qdt,size", [(torch.float16, 2.0 ** -16), (torch.float16, 2.0 ** -22), (torch.bfloat16, 2.0 ** -60),
+                                      (torch.bfloat16, 2.0 ** 90)])
+@pytest.mark.parametrize("times", [1, 300])
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 2, 2), (64, 8, 1), (128, 8, 2)])
+def test_very_small_and_large_queries(pa, qdt, size, times, D, Hq, Hkv):
+    """Subnormal elements and far exponents, the scale making up for them."""
+    c = raised(D, Hq, Hkv, 16, [1, 40, 300], times, 62, torch.float32)
+    c.q = (c.q * size).to(qdt).float()
+    c.scale /= size
+    c.check(c.run(pa, qdt), qdt)
+    assert pa.pa_read_device_errors() == 0
